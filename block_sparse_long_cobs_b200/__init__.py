@@ -2,7 +2,7 @@
 
 The functions (``cobs_build_block_stats``, ``cobs_select_blocks``,
 ``cobs_sparse_decode``, ...) forward to the C ABI of ``libcobs_b200.so``
-(declared in ``include/cobs.h``); see ``_binding.py``.  The library is loaded
+(declared in ``include/cobs.h`` and ``include/cobs_cache.h``); see ``_binding.py``.  The library is loaded
 on first use, and that first use raises ImportError if it has not been built
 (``python -m block_sparse_long_cobs_b200.build``): there is no fallback path.
 """
@@ -20,6 +20,10 @@ __all__ = [
     "cobs_sparse_decode_varlen", "cobs_build_block_stats_paged", "cobs_sparse_decode_paged",
     "cobs_read_device_status", "cobs_no_alloc_read_status", "cobs_set_wait_limit_ns",
     "cobs_last_error", "cobs_status_string",
+    "cobs_kv_cache", "cobs_rope", "cobs_rope_init", "cobs_append_tokens", "cobs_read_cache",
+    "cobs_prompt_workspace_bytes", "cobs_prompt_attention", "cobs_sparse_decode_cache",
+    "COBS_CACHE_BF16", "COBS_CACHE_E4M3", "COBS_ROPE_PLAIN", "COBS_ROPE_LINEAR",
+    "COBS_ROPE_BY_PARTS", "COBS_ROPE_CUSTOM",
     "COBS_OK", "COBS_ERR_INVALID_ARG", "COBS_ERR_UNSUPPORTED",
     "COBS_ERR_WORKSPACE", "COBS_ERR_CUDA", "COBS_ERR_TIMEOUT", "COBS_ERR_DEVICE",
 ]

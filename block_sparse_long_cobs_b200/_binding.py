@@ -1,4 +1,4 @@
-"""Thin Python binding of the COBS block-sparse decode C ABI (``include/cobs.h``).
+"""Thin Python binding of the COBS C ABI (``include/cobs.h``, ``include/cobs_cache.h``).
 
 Argument marshalling only: every function here forwards to the function of
 the same name in ``libcobs_b200.so`` (built in-tree by
@@ -27,6 +27,10 @@ __all__ = [
     "cobs_set_wait_limit_ns",
     "cobs_last_error",
     "cobs_status_string",
+    "cobs_kv_cache", "cobs_rope", "cobs_rope_init", "cobs_append_tokens", "cobs_read_cache",
+    "cobs_prompt_workspace_bytes", "cobs_prompt_attention", "cobs_sparse_decode_cache",
+    "COBS_CACHE_BF16", "COBS_CACHE_E4M3", "COBS_ROPE_PLAIN", "COBS_ROPE_LINEAR",
+    "COBS_ROPE_BY_PARTS", "COBS_ROPE_CUSTOM",
     "COBS_OK", "COBS_ERR_INVALID_ARG", "COBS_ERR_UNSUPPORTED",
     "COBS_ERR_WORKSPACE", "COBS_ERR_CUDA", "COBS_ERR_TIMEOUT", "COBS_ERR_DEVICE",
 ]
@@ -45,6 +49,14 @@ COBS_STATS_BF16 = 0     # block records: mu and U in bf16
 COBS_STATS_FP4 = 1      # block records: mu in bf16, U in scaled FP4 (E2M1)
 COBS_STATS_BOX = 2      # block records: per-dimension min and max of the keys (bf16)
 COBS_STATS_SUBSPACE = 3  # block records: mu in bf16, U projected on a query subspace (bf16)
+
+COBS_CACHE_BF16 = 0     # KV cache: keys and values in bf16
+COBS_CACHE_E4M3 = 1     # KV cache: E4M3 codes and one fp32 scale per row
+
+COBS_ROPE_PLAIN = 0     # rotary frequencies base^(-2 t / rotary_dim)
+COBS_ROPE_LINEAR = 1    # ... divided by factor
+COBS_ROPE_BY_PARTS = 2  # ... slow pairs divided by factor, fast ones kept
+COBS_ROPE_CUSTOM = 3    # given frequencies
 
 
 class CobsError(RuntimeError):
@@ -70,6 +82,55 @@ class cobs_dims(ctypes.Structure):
     ]
 
 
+class cobs_kv_cache(ctypes.Structure):
+    """A KV cache as the cache calls take it (``include/cobs_cache.h``).  Buffers
+    are given as in the calls (CUDA tensors, addresses or None); the descriptor
+    keeps the tensors alive."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("table_stride", ctypes.c_int32),
+        ("format", ctypes.c_int32),             # COBS_CACHE_BF16 / _E4M3
+    ]
+
+    def __init__(self, k=None, v=None, k_scale=None, v_scale=None, block_table=None, n_pages=0,
+                 table_stride=0, format=COBS_CACHE_BF16):
+        super().__init__(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                         n_pages, table_stride, format)
+        self._buffers = (k, v, k_scale, v_scale, block_table)
+
+
+class cobs_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),            # COBS_ROPE_*
+        ("reserved", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_context", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("attention_factor", ctypes.c_double),
+        ("frequencies", ctypes.POINTER(ctypes.c_double)),
+    ]
+
+
+class cobs_rope(ctypes.Structure):
+    """A rotary table, made by cobs_rope_init."""
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("attention_factor", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("turns", ctypes.c_uint64 * 64),        # turns per token of a pair, times 2^64
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -78,7 +139,7 @@ def _load() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, F32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                             ctypes.c_size_t, ctypes.c_float)
-    D = ctypes.POINTER(cobs_dims)
+    D, C = ctypes.POINTER(cobs_dims), ctypes.POINTER(cobs_kv_cache)
     sig = {
         "cobs_abi_version": (I32, []),
         "cobs_stats_record_bytes": (I64, [D]),
@@ -100,6 +161,13 @@ def _load() -> ctypes.CDLL:
         "cobs_read_device_status": (I32, [P, SZ, ctypes.POINTER(I32), P]),
         "cobs_no_alloc_read_status": (I32, [ctypes.POINTER(I32), P]),
         "cobs_set_wait_limit_ns": (I32, [ctypes.c_uint64]),
+        "cobs_rope_init": (I32, [ctypes.POINTER(cobs_rope_params), ctypes.POINTER(cobs_rope)]),
+        "cobs_append_tokens": (I32, [D, C, ctypes.POINTER(cobs_rope), P, I64, P, I64, P, I64, P,
+                                     I64, P, P, P, SZ, P]),
+        "cobs_read_cache": (I32, [D, C, P, I64, I64, P, P, P, SZ, P]),
+        "cobs_prompt_workspace_bytes": (SZ, [D, I64, I64]),
+        "cobs_prompt_attention": (I32, [D, C, P, P, I64, P, I64, F32, P, P, P, SZ, P]),
+        "cobs_sparse_decode_cache": (I32, [D, C, P, P, P, I32, P, I64, F32, P, P, P, SZ, P]),
         "cobs_last_error": (ctypes.c_char_p, []),
         "cobs_status_string": (ctypes.c_char_p, [I32]),
     }
@@ -314,3 +382,92 @@ def cobs_set_wait_limit_ns(limit_ns: int) -> int:
     """Limit of the statistics kernel's first bounded device wait (0: the
     default 2 s); a testing and diagnostic knob."""
     return _check("cobs_set_wait_limit_ns", lib.cobs_set_wait_limit_ns(int(limit_ns)), True)
+
+
+def _rows_ptr(x, stride, name):
+    """Address of packed rows that start ``stride`` elements apart: a CUDA
+    tensor whose rows are contiguous and lie that far apart (a part of a fused
+    projection), an address or None."""
+    if not hasattr(x, "data_ptr"):
+        return _ptr(x)
+    if not x.is_cuda:
+        raise TypeError("tensor arguments must be CUDA tensors (got a host tensor)")
+    if x.shape[0] > 1 and x.stride(0) != stride or x.shape[0] > 0 and not x[0].is_contiguous():
+        raise TypeError(f"{name}: rows must be contiguous and {name}_stride elements apart")
+    return x.data_ptr()
+
+
+def cobs_rope_init(rotary_dim, interleaved=False, base=10000.0, scaling=COBS_ROPE_PLAIN,
+                   factor=1.0, original_context=0.0, low=0.0, high=0.0, attention_factor=1.0,
+                   frequencies=None) -> cobs_rope:
+    """Rotary table of ``rotary_dim`` leading dimensions (host work only)."""
+    f = None
+    if frequencies is not None:
+        f = [float(x) for x in frequencies]
+        if len(f) < rotary_dim // 2:
+            raise ValueError("frequencies: one per rotated pair is needed")
+        f = (ctypes.c_double * len(f))(*f)
+    p = cobs_rope_params(rotary_dim, int(interleaved), scaling, 0, base, factor,
+                         original_context, low, high, attention_factor, f)
+    rope = cobs_rope()
+    _check("cobs_rope_init", lib.cobs_rope_init(ctypes.byref(p), ctypes.byref(rope)), True)
+    return rope
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def cobs_append_tokens(dims, cache, rope, q, q_stride, k, k_stride, v, v_stride, cu_tokens,
+                       n_tokens, start, q_out, ws, ws_bytes, stream=None, check=True) -> int:
+    """Rotate the packed new tokens' q and k and store their k and v in the cache.
+    q, k and v may be parts of one fused projection (rows q_stride, ... apart);
+    rope and q (with q_out) may be None."""
+    st = lib.cobs_append_tokens(ctypes.byref(_dims(dims)), _ref(cache), _ref(rope),
+                                _rows_ptr(q, q_stride, "q"), q_stride,
+                                _rows_ptr(k, k_stride, "k"), k_stride,
+                                _rows_ptr(v, v_stride, "v"), v_stride, _ptr(cu_tokens),
+                                n_tokens, _ptr(start), _ptr(q_out), _ptr(ws), ws_bytes,
+                                _stream(stream))
+    return _check("cobs_append_tokens", st, check)
+
+
+def cobs_read_cache(dims, cache, seq_lens, block_begin, block_end, k_out, v_out, ws, ws_bytes,
+                    stream=None, check=True) -> int:
+    """Blocks of a cache of either format as bf16 pages (seq_lens, k_out or v_out
+    may be None)."""
+    st = lib.cobs_read_cache(ctypes.byref(_dims(dims)), _ref(cache), _ptr(seq_lens),
+                             block_begin, block_end, _ptr(k_out), _ptr(v_out), _ptr(ws),
+                             ws_bytes, _stream(stream))
+    return _check("cobs_read_cache", st, check)
+
+
+def cobs_prompt_workspace_bytes(dims, n_tokens, max_seq_len) -> int:
+    n = lib.cobs_prompt_workspace_bytes(ctypes.byref(_dims(dims)), n_tokens, max_seq_len)
+    if n == 0:
+        raise CobsError("cobs_prompt_workspace_bytes", COBS_ERR_INVALID_ARG, cobs_last_error())
+    return n
+
+
+def cobs_prompt_attention(dims, cache, q, cu_tokens, n_tokens, seq_lens, max_seq_len,
+                          softmax_scale, out, lse, ws, ws_bytes, stream=None,
+                          check=True) -> int:
+    """Causal attention of the packed new tokens over the bf16 cache that holds
+    them (cu_tokens None: one token per sequence; lse may be None)."""
+    st = lib.cobs_prompt_attention(ctypes.byref(_dims(dims)), _ref(cache), _ptr(q),
+                                   _ptr(cu_tokens), n_tokens, _ptr(seq_lens), max_seq_len,
+                                   softmax_scale, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                   _stream(stream))
+    return _check("cobs_prompt_attention", st, check)
+
+
+def cobs_sparse_decode_cache(dims, cache, q, idx, n_sel, idx_stride, seq_lens, max_seq_len,
+                             softmax_scale, out, lse, ws, ws_bytes, stream=None,
+                             check=True) -> int:
+    """cobs_sparse_decode over a cache of either format, contiguous or paged
+    (seq_lens None: every sequence is max_seq_len tokens long)."""
+    st = lib.cobs_sparse_decode_cache(ctypes.byref(_dims(dims)), _ref(cache), _ptr(q),
+                                      _ptr(idx), _ptr(n_sel), idx_stride, _ptr(seq_lens),
+                                      max_seq_len, softmax_scale, _ptr(out), _ptr(lse),
+                                      _ptr(ws), ws_bytes, _stream(stream))
+    return _check("cobs_sparse_decode_cache", st, check)

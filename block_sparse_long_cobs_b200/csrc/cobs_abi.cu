@@ -9,12 +9,14 @@
 #include <cstdio>
 #include <string>
 
-#include "cobs_internal.h"
+#include "abi_common.h"
 
 namespace cobs {
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
 
 cobs_status fail(cobs_status st, const char* fmt, ...) {
   char buf[512];
@@ -34,11 +36,6 @@ cobs_status ok() {
 cobs_status cuda_fail(cudaError_t e, const char* what) {
   return fail(COBS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 cobs_status check_dims(const cobs_dims* d) {
   if (!d) return fail(COBS_ERR_INVALID_ARG, "dims is NULL");
@@ -80,6 +77,8 @@ cobs_status check_dims(const cobs_dims* d) {
   return COBS_OK;
 }
 
+namespace {
+
 int64_t record_bytes(const cobs_dims* d) {
   return stats_record_bytes(d->head_dim, d->rank, d->stats_format,
                             d->stats_format == COBS_STATS_SUBSPACE ? d->subspace_dim : 0);
@@ -98,6 +97,8 @@ int32_t selected_capacity(const cobs_dims* d, int32_t top_k, int32_t sink, int32
   const int64_t want = int64_t(top_k) + sink + ceil_div(local, kBlock) + 1;
   return int32_t(want < nb ? want : nb);
 }
+
+}  // namespace
 
 WorkspaceLayout layout(const cobs_dims* d, int32_t n_sel_max) {
   WorkspaceLayout L{};
@@ -122,9 +123,6 @@ WorkspaceLayout layout(const cobs_dims* d, int32_t n_sel_max) {
   return L;
 }
 
-// Smallest layout that still holds the status word (build_block_stats).
-constexpr size_t kStatusBytes = 256;
-
 cobs_status check_ws(void* ws, size_t have, size_t need) {
   if (!ws) return fail(COBS_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned16(ws)) return fail(COBS_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
@@ -133,8 +131,6 @@ cobs_status check_ws(void* ws, size_t have, size_t need) {
                 need);
   return COBS_OK;
 }
-
-}  // namespace
 
 namespace {
 std::atomic<uint64_t> g_wait_limit_ns{0};   // 0: the default limit
@@ -277,13 +273,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   return a.d == 128 ? launch_decode_tc(a, stream) : launch_decode_d64(a, stream);
 }
 
-}  // namespace cobs
-
-using namespace cobs;
-
-// block_table null: the contiguous cache [batch, Hkv, capacity_tokens, d];
-// else a page pool [n_pages, Hkv, 64, d] addressed through the table.
-static cobs_status check_paging(const cobs_dims* dims, const int32_t* block_table,
+cobs_status check_paging(const cobs_dims* dims, const int32_t* block_table,
                                 int32_t table_stride, int64_t n_pages, int64_t blocks_needed) {
   if (!block_table) return COBS_OK;
   if (!aligned16(block_table))
@@ -298,6 +288,10 @@ static cobs_status check_paging(const cobs_dims* dims, const int32_t* block_tabl
     return fail(COBS_ERR_UNSUPPORTED, "batch * table_stride must be < 2^31");
   return COBS_OK;
 }
+
+}  // namespace cobs
+
+using namespace cobs;
 
 static cobs_status stats_impl(const cobs_dims* dims, const void* k, const int32_t* block_table,
                               int32_t table_stride, int64_t n_pages, int64_t block_begin,
@@ -606,6 +600,23 @@ static cobs_status decode_impl(const cobs_dims* dims, const void* q, const void*
   if (e != cudaSuccess) return cuda_fail(e, "sparse decode launch");
   return ok();
 }
+
+}  // extern "C"
+
+namespace cobs {
+
+cobs_status decode_args(const cobs_dims* dims, const void* q, const void* k, const void* v,
+                        const int32_t* block_table, int32_t table_stride, int64_t n_pages,
+                        const int32_t* idx, const int32_t* n_sel, int32_t idx_stride,
+                        const int64_t* seq_lens, int64_t seq_len, float softmax_scale,
+                        float* out, float* lse, void* ws, size_t ws_bytes, DecodeArgs* args) {
+  return decode_impl(dims, q, k, v, block_table, table_stride, n_pages, idx, n_sel, idx_stride,
+                     seq_lens, seq_len, softmax_scale, out, lse, ws, ws_bytes, nullptr, args);
+}
+
+}  // namespace cobs
+
+extern "C" {
 
 cobs_status cobs_sparse_decode(const cobs_dims* dims, const void* q, const void* k,
                                const void* v, const int32_t* idx, const int32_t* n_sel,
