@@ -1,101 +1,843 @@
 // Causal attention of packed new tokens over the bf16 cache
-// (include/cobs_cache.h, cobs_prompt_attention).
+// (include/cobs_cache.h, cobs_prompt_attention) on the 5th-generation tensor
+// cores.
 //
-// One warp per (token, query head): the keys of 32 tokens at a time, one per
-// lane, then p = 2^(s - m) with a running maximum m and sum l, and the values
-// summed with the output dimensions spread over the lanes.
+//   out_r = sum_{j <= p_r} e^(s_rj - m_r) v_j / sum_j e^(s_rj - m_r),
+//   s_rj = softmax_scale q_r . k_j,
+// in one pass over the keys with a running maximum m and sum l per row.
+//
+// Tiles.  The G query heads of a kv-head share its keys, so a tile's 128 rows
+// are 128 / G tokens x G heads; a unit of work is two such tiles (consecutive
+// tokens of one sequence and kv-head) against all keys up to the unit's last
+// position, 128 keys per iteration.  Per iteration and tile the tensor cores
+// form S = Q K^T (M = 128 rows, N = 128 keys) and O += P V (P read from
+// tensor memory).  The two tiles alternate: while one tile's P is formed the
+// tensor cores work for the other, so that neither waits.
+//   warps 0-3, 4-7  softmax of tile 0, 1: one row per thread.  p = 2^(s - m)
+//                   with m raised only when a row's logit exceeds it by more
+//                   than 2^8 (the warp then rescales its rows of O in tensor
+//                   memory; the products that wrote them were issued before
+//                   the ones that made S, so they are complete).  P
+//                   overwrites S as bf16.  No barrier among warps: a row
+//                   belongs to one thread from the scores to the output.
+//   warp 8          schedule and TMA: Q once per unit, K_i, V_i through a ring
+//   warp 9          issues the products
+//
+// Work split.  The iterations of all units, laid end to end, are cut into
+// equal shares, one per CTA (one CTA per SM), so that ragged lengths, causal
+// triangles and a few rows over a long context all fill the GPU evenly.  A
+// unit that a cut goes through leaves partial rows (o, m, l) in the workspace
+// (at most two per CTA), which prompt_merge_kernel joins.  With sequences of
+// at most kWholeTokens tokens the shares are whole units instead: cutting them
+// would cost more than it evens out.
+//
+// Rows of the last block past a sequence's end are zeroed in the V tile after
+// it lands (a zero weight times a NaN is not zero); scores of keys past a
+// row's position are masked whatever the key holds.  Every wait is bounded;
+// a CTA that gives up records COBS_ERR_TIMEOUT, lets its copies and products
+// finish, frees its tensor memory and returns.
 #include "cache_device.cuh"
+#include "tcgen05.cuh"
 
 namespace cobs {
 namespace {
 
-constexpr int kPromptWarps = 4;
+constexpr int kThreads = 384;            // two softmax warpgroups, one for the rest
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+// Registers: 384 x 168 at launch, of which the softmax threads (a row of 128
+// scores each) take 208 and the others keep 80.
+constexpr int kSoftRegs = 208, kOtherRegs = 80;
+static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "register split");
+constexpr int kTileRows = 128;
+constexpr int kKeys = 128;               // keys per iteration
+constexpr int kUnitRows = 2 * kTileRows;
+constexpr int kMaxCtas = 148;            // one per SM
+constexpr int64_t kWholeTokens = 1024;   // longest sequence whose units are never cut
+constexpr int kMinShare = 4;             // iterations of a share, at least
+constexpr int kSegQ = 2;                 // segments handed from the producer to the others
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kTmemCols = 512;      // S0, S1 (P over them), O0, O1
+constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kPromptWarps) prompt_rows_kernel(const PromptArgs a) {
-  constexpr int kE = D / 32;   // output dimensions of a lane
-  __shared__ float qs[kPromptWarps][D];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = int64_t(blockIdx.x) * kPromptWarps + warp;
-  const int64_t token = row / a.hq;
-  const int hq = int(row % a.hq);
-  if (token >= a.n_tokens) return;
-  const int b = warp_find_sequence(a.cu, a.batch, token, lane);
-  if (b >= a.batch) return;
-  const int kvh = hq / (a.hq / a.c.hkv);
-  int64_t len = __ldg(a.seq_lens + b);
-  if (len < 0 || len > a.max_seq_len) {
-    if (lane == 0) report(a.status, COBS_ERR_DEVICE);
-    len = len < 0 ? 0 : a.max_seq_len;
+struct Tile {
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kSlabBytes = 128 * 128;          // 128 rows x 64 columns bf16
+  static constexpr int kBytes = kSlabs * kSlabBytes;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffQ = kStages * kBytes;
+  static constexpr int kDynSmem = kOffQ + 2 * kBytes + 1024;
+};
+
+// How a segment covers its unit.
+enum SegType : int32_t { kNone = 0, kWhole = 1, kBegin = 2, kMiddle = 3, kEnd = 4 };
+
+struct Segment {
+  int64_t tok0;    // first packed row
+  int64_t pos0;    // its position
+  int64_t len;     // tokens of the sequence
+  int32_t b, h;    // sequence, kv-head
+  int32_t ntok;    // tokens of the unit
+  int32_t it0, it1;
+  int32_t type;
+};
+
+// What a CTA leaves in the workspace beside its partial rows: slot 0 its
+// first segment when that does not begin its unit, slot 1 its last when that
+// begins one without ending it.
+struct SlotNote {
+  int64_t tok0;
+  int32_t ntok, h;
+  int32_t type, pad;
+};
+
+__host__ __device__ inline int64_t floor_div(int64_t a, int64_t b) {
+  const int64_t q = a / b;
+  return a % b != 0 && (a < 0) != (b < 0) ? q - 1 : q;
+}
+__host__ __device__ inline int64_t div_up(int64_t a, int64_t b) { return -floor_div(-a, b); }
+
+// Units of one sequence and kv-head: count rows at positions [len - count,
+// len), `k` tokens per unit.  A unit's iterations cover the keys up to its
+// last position, one iteration at least (rows before the sequence's start
+// have no key and still need their outputs).
+struct SeqUnits {
+  int64_t c, count, len;   // c = len - count
+  int32_t k;
+  __host__ __device__ int64_t units() const { return (count + k - 1) / k; }
+  __host__ __device__ int64_t iters(int64_t u) const {
+    const int64_t end = c + (u + 1) * k < len ? c + (u + 1) * k : len;
+    const int64_t n = div_up(end, kKeys);
+    return n > 1 ? n : 1;
   }
-  const int64_t last = a.cu != nullptr ? __ldg(a.cu + b + 1) : token + 1;
-  const int64_t pos = len - (last - token);
-  for (int t = lane; t < D; t += 32)
-    qs[warp][t] = __uint_as_float(uint32_t(a.q[row * D + t]) << 16);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = 0.f;
-  for (int64_t j0 = 0; j0 <= pos; j0 += 32) {
-    const int64_t r0 = cache_row(a.c, b, kvh, j0);
-    if (r0 < 0) {
-      if (lane == 0) report(a.status, COBS_ERR_DEVICE);
-      continue;
+  // Iterations of the first n units.  For a full unit j = u + 1 they are
+  // max(1, ceil((c + k j) / 128)); with k = 128 / m this is ceil((c' + j) / m),
+  // c' = ceil(c / k), and with k = 128 s it is ceil(c / 128) + s j.
+  __host__ __device__ int64_t before(int64_t n) const {
+    int64_t extra = 0;
+    if (n > 0 && n == units()) {   // the last unit may be short
+      --n;
+      extra = iters(n);
     }
-    const int n = int(pos + 1 - j0 < 32 ? pos + 1 - j0 : 32);
-    float s = -INFINITY;
-    if (lane < n) {
-      const uint4* kp = reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(a.c.k) + (r0 + lane) * D);
-      float acc = 0.f;
-#pragma unroll 4
-      for (int t = 0; t < D / 8; ++t) {
-        const uint4 w = kp[t];
-        const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+    if (n <= 0) return extra;
+    if (k < kKeys) {
+      const int64_t m = kKeys / k, cp = div_up(c, k);
+      int64_t n0 = -cp < 0 ? 0 : (-cp > n ? n : -cp);   // units with no key: 1 each
+      auto f = [m](int64_t x) {   // sum of ceil(y / m) over y = 1 .. x
+        const int64_t q = x / m, r = x % m;
+        return m * (q * (q + 1) / 2) + r * (q + 1);
+      };
+      if (n0 == n) return extra + n;
+      return extra + n0 + f(cp + n) - f(cp > 0 ? cp : 0);
+    }
+    const int64_t s = k / kKeys, cp = div_up(c, kKeys);
+    int64_t n0 = floor_div(-cp, s);
+    n0 = n0 < 0 ? 0 : (n0 > n ? n : n0);
+    return extra + n0 + (n - n0) * cp + s * (n * (n + 1) - n0 * (n0 + 1)) / 2;
+  }
+  // Shares are counted in units (whole) or in iterations.
+  __host__ __device__ int64_t weight(bool whole) const { return whole ? units() : before(units()); }
+};
+
+__device__ __forceinline__ SeqUnits seq_units(const PromptArgs& a, int64_t b, int k,
+                                              bool reporter) {
+  SeqUnits s;
+  s.k = k;
+  s.count = a.cu != nullptr ? int64_t(__ldg(a.cu + b + 1)) - __ldg(a.cu + b) : 1;
+  if (s.count < 0) s.count = 0;
+  s.len = __ldg(a.seq_lens + b);
+  if (s.len < 0 || s.len > a.max_seq_len) {
+    if (reporter && s.count > 0) report(a.status, COBS_ERR_DEVICE);
+    s.len = s.len < 0 ? 0 : a.max_seq_len;
+  }
+  s.c = s.len - s.count;
+  return s;
+}
+
+// D[tmem] (+)= A[tmem] B: A is bf16, two per column.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float2 f = bf16x2_to_float2(wv[u]);
-          acc = fmaf(f.x, qs[warp][8 * t + 2 * u], acc);
-          acc = fmaf(f.y, qs[warp][8 * t + 2 * u + 1], acc);
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+constexpr size_t slot_floats(int d) { return size_t(kUnitRows) * (d + 2); }
+
+// Partial rows of a slot: o as [D / 4][256 rows][4], then m [256], l [256],
+// so that a warp's 32 rows write and read whole lines.
+__device__ __forceinline__ float* slot_rows(const PromptArgs& a, int d, int64_t slot) {
+  return a.partials + kMaxCtas * 2 * (sizeof(SlotNote) / 4) + slot * slot_floats(d);
+}
+__device__ __forceinline__ SlotNote* slot_note(const PromptArgs& a, int64_t slot) {
+  return reinterpret_cast<SlotNote*>(a.partials) + slot;
+}
+
+// Wait of a whole warp; false (for every lane) when it ran out.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status,
+                                          volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, status, abort_flag));
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+              const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PromptArgs a) {
+  using T = Tile<D>;
+  constexpr int kStages = T::kStages;
+  extern __shared__ uint8_t dyn_smem[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[kStages];
+  __shared__ __align__(8) uint64_t empty[kStages];
+  __shared__ __align__(8) uint64_t q_full, q_empty, v_tail, drain;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2];
+  __shared__ __align__(8) uint64_t seg_full[kSegQ], seg_empty[kSegQ];
+  __shared__ Segment seg_q[kSegQ];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_s;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.hq / a.c.hkv;
+  const int tt = kTileRows / group;        // tokens of a tile
+
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&v_tail, 1);
+    mbar_init(&drain, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&s_full[w], 1);
+      mbar_init(&p_full[w], 4);
+      mbar_init(&o_full[w], 1);
+    }
+    for (int s = 0; s < kSegQ; ++s) {
+      mbar_init(&seg_full[s], 1);
+      mbar_init(&seg_empty[s], 9);
+    }
+    fence_barrier_init();
+    abort_s = 0;
+  }
+  if (warp == 0) tmem_alloc(&tmem_slot, kTmemCols);
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp >= kProducerWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kProducerWarp) {
+    // ==================== schedule and TMA (whole warp) ====================
+    const bool whole = a.max_seq_len <= kWholeTokens;
+    const int k_unit = 2 * tt;
+    const int hkv = a.c.hkv;
+    // this CTA's share [t0, t1) of the work
+    int64_t total = 0;
+    for (int64_t b = lane; b < a.batch; b += 32)
+      total += seq_units(a, b, k_unit, blockIdx.x == 0).weight(whole);
+    total = warp_sum64(total) * hkv;
+    int64_t n = whole ? total : total / kMinShare;
+    n = n < 1 ? 1 : (n > int64_t(gridDim.x) ? int64_t(gridDim.x) : n);
+    int64_t t0 = 0, t1 = 0;
+    if (int64_t(blockIdx.x) < n) {
+      t0 = total * int64_t(blockIdx.x) / n;
+      t1 = total * (int64_t(blockIdx.x) + 1) / n;
+    }
+    // the sequence, kv-head and unit of t0
+    int64_t b = 0, skipped = 0, w_b = 0;
+    SeqUnits su{};
+    for (int64_t b0 = 0; b0 < a.batch && t0 < t1; b0 += 32) {
+      const int64_t mine = b0 + lane < a.batch ? b0 + lane : a.batch - 1;
+      const int64_t wgt =
+          b0 + lane < a.batch ? seq_units(a, mine, k_unit, false).weight(whole) * hkv : 0;
+      int64_t inc = wgt;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m) inc += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, skipped + inc > t0);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        b = b0 + l;
+        w_b = __shfl_sync(0xffffffffu, wgt, l);
+        skipped += __shfl_sync(0xffffffffu, inc - wgt, l);
+        break;
+      }
+      skipped += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    int64_t h = 0, u = 0, it = 0;
+    if (t0 < t1) {
+      su = seq_units(a, b, k_unit, false);
+      const int64_t w_h = w_b / hkv;
+      h = (t0 - skipped) / w_h;
+      const int64_t rest = (t0 - skipped) % w_h;
+      if (whole) {
+        u = rest;
+      } else {
+        int64_t lo = 0, hi = su.units() - 1;   // the last u with before(u) <= rest
+        while (lo < hi) {
+          const int64_t mid = (lo + hi + 1) / 2;
+          if (su.before(mid) <= rest) lo = mid;
+          else hi = mid - 1;
+        }
+        u = lo;
+        it = rest - su.before(u);
+      }
+    }
+    uint32_t item = 0;       // ring items issued
+    uint32_t tails = 0;      // uses of v_tail
+    uint32_t nseg = 0;
+    SlotNote note[2] = {};
+    bool ok = true;
+    int64_t left = t1 - t0;
+    while (left > 0 && ok) {
+      const int64_t n_it = su.iters(u);
+      Segment g;
+      g.b = int32_t(b);
+      g.h = int32_t(h);
+      g.tok0 = (a.cu != nullptr ? int64_t(__ldg(a.cu + b)) : b) + u * k_unit;
+      g.pos0 = su.c + u * k_unit;
+      g.len = su.len;
+      g.ntok = int32_t(su.count - u * k_unit < k_unit ? su.count - u * k_unit : k_unit);
+      g.it0 = int32_t(it);
+      g.it1 = int32_t(whole || n_it - it <= left ? n_it : it + left);
+      const bool first = g.it0 == 0, last = g.it1 == n_it;
+      g.type = first ? (last ? kWhole : kBegin) : (last ? kEnd : kMiddle);
+      if (g.type != kWhole) {
+        SlotNote& nt = note[g.type == kBegin ? 1 : 0];
+        nt.tok0 = g.tok0;
+        nt.ntok = g.ntok;
+        nt.h = g.h;
+        nt.type = g.type;
+      }
+      left -= whole ? 1 : g.it1 - g.it0;
+      // ---- hand the segment over ----
+      const int qs = nseg % kSegQ;
+      if (nseg >= kSegQ &&
+          !warp_wait(&seg_empty[qs], ((nseg / kSegQ) - 1) & 1, a.status, &abort_s))
+        break;
+      if (lane == 0) {
+        seg_q[qs] = g;
+        mbar_arrive(&seg_full[qs]);
+      }
+      // ---- the unit's queries ----
+      if (nseg > 0 && !warp_wait(&q_empty, (nseg - 1) & 1, a.status, &abort_s)) break;
+      ++nseg;
+      const int tiles = g.ntok > tt ? 2 : 1;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full, uint32_t(tiles * T::kBytes));
+        for (int w = 0; w < tiles; ++w)
+          for (int s = 0; s < T::kSlabs; ++s)
+            tma_load_3d(base + T::kOffQ + w * T::kBytes + s * T::kSlabBytes, &qmap, 64 * s,
+                        g.h * group, int(g.tok0 + w * tt), &q_full);
+      }
+      // ---- keys and values ----
+      const int64_t blocks = (g.len + kBlock - 1) / kBlock;
+      const int64_t rows_bound = (a.max_seq_len + kBlock - 1) / kBlock * kBlock;
+      int32_t page = -1;     // page of block pg0 + lane
+      int64_t pg0 = -64;
+      for (int i = g.it0; i < g.it1 && ok; ++i) {
+        int y[2], z[2];
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const int64_t j = 2 * int64_t(i) + h2;
+          bool in = j < blocks;
+          if constexpr (kPaged) {
+            if (j >= pg0 + 32 || j < pg0) {
+              pg0 = j;
+              const int64_t jj = j + lane;
+              page = jj < blocks ? __ldg(a.c.table + b * a.c.table_stride + jj) : -1;
+            }
+            const int32_t p = __shfl_sync(0xffffffffu, page, int(j - pg0));
+            const bool good = p >= 0 && p < a.c.n_pages;
+            if (in && !good && lane == 0) report(a.status, COBS_ERR_DEVICE);
+            in = in && good;
+            y[h2] = in ? 0 : kBlock;       // past the map's rows: reads as zero
+            z[h2] = in ? int(int64_t(p) * hkv + g.h) : 0;
+          } else {
+            y[h2] = in ? int(j * kBlock) : int(rows_bound);
+            z[h2] = int(g.b * hkv + g.h);
+          }
+        }
+        // rows of the sequence's last block past its end hold anything
+        const int64_t tail_j = g.len % kBlock != 0 ? blocks - 1 : -1;
+        const bool tail = tail_j >= 0 && (tail_j == 2 * int64_t(i) || tail_j == 2 * int64_t(i) + 1);
+        for (int kv = 0; kv < 2; ++kv, ++item) {
+          const int st = item % kStages;
+          if (item >= kStages &&
+              !warp_wait(&empty[st], ((item / kStages) - 1) & 1, a.status, &abort_s)) {
+            ok = false;
+            break;
+          }
+          uint64_t* bar = kv == 1 && tail ? &v_tail : &full[st];
+          uint8_t* dst = base + st * T::kBytes;
+          if (lane == 0) {
+            const CUtensorMap* map = kv ? &vmap : &kmap;
+            mbar_arrive_expect_tx(bar, uint32_t(T::kBytes));
+            for (int h2 = 0; h2 < 2; ++h2)
+              for (int s = 0; s < T::kSlabs; ++s)
+                tma_load_3d(dst + s * T::kSlabBytes + h2 * 8192, map, 64 * s, y[h2], z[h2], bar);
+          }
+          if (kv == 1 && tail) {
+            if (!warp_wait(&v_tail, tails & 1, a.status, &abort_s)) {
+              (void)mbar_wait_bounded(&v_tail, tails & 1, a.status);   // let it land
+              ok = false;
+              ++item;
+              break;
+            }
+            ++tails;
+            const int r0 = int(tail_j - 2 * int64_t(i)) * 64 + int(g.len % kBlock);
+            const int r1 = int(tail_j - 2 * int64_t(i)) * 64 + 64;
+            for (int e = lane; e < (r1 - r0) * 8; e += 32) {
+#pragma unroll
+              for (int s = 0; s < T::kSlabs; ++s)
+                *reinterpret_cast<uint4*>(dst + s * T::kSlabBytes + r0 * 128 + e * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+          }
         }
       }
-      s = acc * a.scale_log2;
+      if (!ok) break;
+      // ---- the next unit ----
+      it = 0;
+      if (g.it1 == n_it && ++u >= su.units()) {
+        u = 0;
+        if (++h >= hkv) {
+          h = 0;
+          do {
+            ++b;
+            if (b < a.batch) su = seq_units(a, b, k_unit, false);
+          } while (b < a.batch && su.count == 0);
+          if (b >= a.batch) left = 0;
+        }
+      }
     }
-    const float mn = fmaxf(m, warp_max(s));
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn);
-    const float p = lane < n ? exp2f(s - mn) : 0.f;
-    l = l * alpha + warp_sum(p);
-    m = mn;
+    // the end of the work: an empty segment
+    if (ok) {
+      const int qs = nseg % kSegQ;
+      if (nseg < kSegQ || warp_wait(&seg_empty[qs], ((nseg / kSegQ) - 1) & 1, a.status, &abort_s)) {
+        if (lane == 0) {
+          seg_q[qs].type = kNone;
+          mbar_arrive(&seg_full[qs]);
+        }
+      }
+    }
+    if (!whole && lane < 2) *slot_note(a, 2 * int64_t(blockIdx.x) + lane) = note[lane];
+    __syncwarp();
+    if (abort_s) {
+      // copies that were issued and that nobody may have waited for
+      if (nseg > 0) (void)mbar_wait_bounded(&q_full, (nseg - 1) & 1, a.status);
+    }
+    for (uint32_t x = item > uint32_t(kStages) ? item - kStages : 0u; x < item; ++x)
+      (void)mbar_wait_bounded(&full[x % kStages], (x / kStages) & 1, a.status);
+  } else if (warp == kMmaWarp) {
+    // ============================= products ================================
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = umma_idesc_bf16(128, kKeys);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
+      const uint32_t q0 = smem_addr(base + T::kOffQ);
+      uint32_t item = 0, nseg = 0;
+      uint32_t np[2] = {0, 0};     // P tiles consumed
+      bool ok = true, issued = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return wait_or_abort(bar, parity, a.status, &abort_s);
+      };
+      // (a descriptor's address field counts 16 bytes; shared memory ends
+      // below 2^18, so adding to it never carries out of its 14 bits)
+      auto qk = [&](int w, uint32_t st) {
+        const uint64_t qd = umma_desc_sw128(q0 + w * T::kBytes);
+        const uint64_t kd = umma_desc_sw128(smem_addr(base + st * T::kBytes));
 #pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] *= alpha;
-    for (int i = 0; i < n; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, p, i);
-      const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) + (r0 + i) * D + lane * kE;
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * T::kSlabBytes + (ks & 3) * 32) >> 4;
+          umma_bf16(tmem + 128u * w, qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[w]);
+        issued = true;
+      };
+      while (ok) {
+        const int qs = nseg % kSegQ;
+        if (!wait(&seg_full[qs], (nseg / kSegQ) & 1)) break;
+        const int type = seg_q[qs].type, ntok = seg_q[qs].ntok;
+        const int n_it = seg_q[qs].it1 - seg_q[qs].it0;
+        mbar_arrive(&seg_empty[qs]);
+        if (type == kNone) break;
+        const int tiles = ntok > tt ? 2 : 1;
+        uint32_t kst = item % kStages;
+        if (!wait(&q_full, nseg & 1) || !wait(&full[kst], (item / kStages) & 1)) break;
+        ++nseg;
+        tc_fence_after();
+#pragma unroll 1
+        for (int w = 0; w < tiles; ++w) qk(w, kst);
+        umma_commit(&empty[kst]);
+        if (n_it == 1) umma_commit(&q_empty);
+        for (int i = 0; i < n_it && ok; ++i) {
+          const uint32_t vi = item + 1, vst = vi % kStages;
+          item += 2;
+          kst = item % kStages;
+          if (!wait(&full[vst], (vi / kStages) & 1)) {
+            ok = false;
+            break;
+          }
+#pragma unroll 1
+          for (int w = 0; w < tiles; ++w) {
+            if (!wait(&p_full[w], np[w] & 1)) {
+              ok = false;
+              break;
+            }
+            ++np[w];
+            tc_fence_after();
+            const uint64_t vd =
+                umma_desc_sw128_mn(smem_addr(base + vst * T::kBytes), T::kSlabBytes);
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        o[e] = fmaf(pi, __uint_as_float(uint32_t(vp[e]) << 16), o[e]);
+            for (int ks = 0; ks < kKeys / 16; ++ks)
+              umma_bf16_ta(tmem + 256u + uint32_t(D) * w, tmem + 128u * w + 8u * ks,
+                           vd + ks * (2048 >> 4), idesc_pv, (i > 0 || ks > 0) ? 1u : 0u);
+            if (w == tiles - 1) umma_commit(&empty[vst]);
+            if (i + 1 == n_it) {
+              umma_commit(&o_full[w]);
+              continue;
+            }
+            if (w == 0) {
+              if (!wait(&full[kst], (item / kStages) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            qk(w, kst);
+          }
+          if (ok && i + 1 < n_it) {
+            umma_commit(&empty[kst]);
+            if (i + 2 == n_it) umma_commit(&q_empty);
+          }
+        }
+      }
+      if (issued) {   // every product must be complete before TMEM is freed
+        umma_commit(&drain);
+        (void)mbar_wait_bounded(&drain, 0, a.status);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ======================= softmax and output ===========================
+    const int w = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;         // of the tile
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + 128u * w;
+    const uint32_t o_addr = tmem + lane_base + 256u + uint32_t(D) * w;
+    const int tok = w * tt + row / group;           // token of the unit
+    const int tok_w = w * tt + (warp & 3) * 32 / group;   // the warp's first
+    uint32_t nseg = 0, ns = 0, no = 0;
+    bool ok = true;
+    for (; ok; ++nseg) {
+      const int qs = nseg % kSegQ;
+      if (!warp_wait(&seg_full[qs], (nseg / kSegQ) & 1, a.status, &abort_s)) break;
+      const Segment g = seg_q[qs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[qs]);
+      if (g.type == kNone) break;
+      if (w == 1 && g.ntok <= tt) continue;
+      const bool busy = tok_w < g.ntok;             // a row of the warp is a token's
+      const int64_t pos = g.pos0 + tok;
+      const int64_t pos_w = g.pos0 + tok_w;
+      float m = -INFINITY, l = 0.f;
+      for (int i = g.it0; i < g.it1; ++i, ++ns) {
+        const int64_t key0 = int64_t(i) * kKeys;
+        // blocks of this iteration without a page (their keys are not there)
+        uint32_t gone = 0;
+        if constexpr (kPaged) {
+          const int64_t j = 2 * int64_t(i) + lane;
+          bool bad = false;
+          if (busy && lane < 2 && j * kBlock < g.len) {
+            const int32_t p = __ldg(a.c.table + int64_t(g.b) * a.c.table_stride + j);
+            bad = p < 0 || p >= a.c.n_pages;
+          }
+          gone = __ballot_sync(0xffffffffu, bad);
+        }
+        if (!warp_wait(&s_full[w], ns & 1, a.status, &abort_s)) {
+          ok = false;
+          break;
+        }
+        if (busy) {
+          tc_fence_after();
+          float s[kKeys];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_addr + 32u * c, s + 32 * c);
+          tmem_wait_ld();
+          if (key0 + kKeys - 1 > pos_w || (kPaged && gone != 0)) {
+            const int64_t room = pos - key0;
+            const int lim = room > kKeys ? kKeys : (room < -1 ? -1 : int(room));
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c) {
+              const bool hide = c > lim || (kPaged && ((gone >> (c >> 6)) & 1u));
+              s[c] = hide ? -INFINITY : s[c];
+            }
+          }
+          float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
+#pragma unroll
+          for (int c = 4; c < kKeys; c += 4) {
+            mx0 = max3(mx0, s[c], s[c + 1]);
+            mx1 = max3(mx1, s[c + 2], s[c + 3]);
+          }
+          const float mx = fmaxf(mx0, mx1) * a.scale_log2;
+          const bool raise = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float mn = raise ? mx : m;
+            const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
+            m = mn;
+            l *= alpha;
+            if (i > g.it0) {
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(o_addr + c, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                tmem_st32(o_addr + c, reinterpret_cast<const uint32_t*>(o));
+              }
+            }
+          }
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          float sum0 = 0.f, sum1 = 0.f;
+          uint32_t p[kKeys / 2];
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 2) {
+            const float p0 = hw_exp2(fmaf(s[c], a.scale_log2, neg_m));
+            const float p1 = hw_exp2(fmaf(s[c + 1], a.scale_log2, neg_m));
+            sum0 += p0;
+            sum1 += p1;
+            p[c / 2] = bf16x2_bits(p0, p1);
+          }
+          l += sum0 + sum1;
+          tmem_st32(s_addr, p);
+          tmem_st32(s_addr + 32u, p + 32);
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+      }
+      if (!ok) break;
+      // ---- the unit's rows (or this segment's part of them) ----
+      if (!warp_wait(&o_full[w], no & 1, a.status, &abort_s)) break;
+      ++no;
+      if (busy) {
+        tc_fence_after();
+        const bool mine = tok < g.ntok;
+        if (g.type == kWhole) {
+          const int64_t r = (g.tok0 + tok) * a.hq + g.h * group + row % group;
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(o_addr + c, o);
+            if (mine) {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + r * D + c);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t v[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  v[x] = l > 0.f ? bf16x2_bits(o[8 * e + 2 * x] * inv, o[8 * e + 2 * x + 1] * inv)
+                                 : 0u;
+                dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+          }
+          if (mine && a.lse != nullptr)
+            a.lse[r] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        } else {
+          float* part = slot_rows(a, D, 2 * int64_t(blockIdx.x) + (g.type == kBegin ? 1 : 0));
+          const int r = w * kTileRows + row;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(o_addr + c, o);
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<float4*>(part)[(c / 4 + e) * kUnitRows + r] =
+                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+          if (mine) {
+            part[kUnitRows * D + r] = m;
+            part[kUnitRows * (D + 1) + r] = l;
+          }
+        }
+        tc_fence_before();
+      }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Units that were cut, joined: the CTA whose last segment begins a unit
+// (slot 1) and the following CTAs' first segments (slot 0) up to the one that
+// ends it.  Block (c, y) joins 16 dimensions of the unit that begins in
+// CTA c, one row per thread:
+//   M = max m_s, L = sum 2^(m_s - M) l_s, out = sum 2^(m_s - M) o_s / L.
+constexpr int kMergeDims = 16;
+template <int D>
+__global__ void __launch_bounds__(kUnitRows) prompt_merge_kernel(const PromptArgs a, int n_ctas) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x;
+  const SlotNote g = *slot_note(a, 2 * int64_t(c) + 1);
+  if (g.type != kBegin) return;
+  const int group = a.hq / a.c.hkv;
+  const int tt = kTileRows / group;
+  const int r = threadIdx.x;
+  const int tok = r / kTileRows * tt + r % kTileRows / group;
+  if (tok >= g.ntok) return;
+  const int d0 = blockIdx.y * kMergeDims;
+  float M = -INFINITY, L = 0.f, o[kMergeDims] = {};
+  int type = kBegin;
+  for (int s = c; s < n_ctas && type != kEnd; ++s) {
+    const int64_t slot = 2 * int64_t(s) + (s == c ? 1 : 0);
+    type = s == c ? int(kBegin) : slot_note(a, slot)->type;
+    const float* part = slot_rows(a, D, slot);
+    const float m = __ldcg(part + kUnitRows * D + r), l = __ldcg(part + kUnitRows * (D + 1) + r);
+    float4 v[kMergeDims / 4];
 #pragma unroll
-  for (int e = 0; e < kE; e += 2)
-    *reinterpret_cast<uint32_t*>(a.out + row * D + lane * kE + e) =
-        bf16x2_bits(o[e] * inv, o[e + 1] * inv);
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+    for (int e = 0; e < kMergeDims / 4; ++e)
+      v[e] = __ldcg(reinterpret_cast<const float4*>(part) + (d0 / 4 + e) * kUnitRows + r);
+    if (m == -INFINITY) continue;
+    const float mn = fmaxf(M, m);
+    const float wo = hw_exp2(M - mn), wn = hw_exp2(m - mn);   // 2^-inf = 0
+    L = L * wo + l * wn;
+#pragma unroll
+    for (int e = 0; e < kMergeDims / 4; ++e) {
+      o[4 * e] = o[4 * e] * wo + v[e].x * wn;
+      o[4 * e + 1] = o[4 * e + 1] * wo + v[e].y * wn;
+      o[4 * e + 2] = o[4 * e + 2] * wo + v[e].z * wn;
+      o[4 * e + 3] = o[4 * e + 3] * wo + v[e].w * wn;
+    }
+    M = mn;
+  }
+  const int64_t row = (g.tok0 + tok) * a.hq + g.h * group + r % group;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint32_t out[kMergeDims / 2];
+#pragma unroll
+  for (int e = 0; e < kMergeDims / 2; ++e) out[e] = bf16x2_bits(o[2 * e] * inv, o[2 * e + 1] * inv);
+#pragma unroll
+  for (int e = 0; e < kMergeDims / 8; ++e)
+    reinterpret_cast<uint4*>(a.out + row * D + d0)[e] =
+        make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
+  if (blockIdx.y == 0 && a.lse != nullptr)
+    a.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+// CTAs of a launch: no more than there can be shares.
+int prompt_ctas(int64_t n_tokens, int batch, int hkv, int group, int64_t max_seq_len) {
+  const int64_t k = 2 * kTileRows / group;
+  const int64_t units = (n_tokens / k + (batch < n_tokens ? batch : n_tokens)) * hkv;
+  const int64_t shares =
+      max_seq_len <= kWholeTokens ? units : units * ((max_seq_len + kKeys - 1) / kKeys);
+  return int(shares < kMaxCtas ? shares : kMaxCtas);
+}
+
+template <int D>
+cudaError_t launch_d(const PromptArgs& a, cudaStream_t stream) {
+  using T = Tile<D>;
+  const int group = a.hq / a.c.hkv;
+  CUtensorMap kmap, vmap, qmap;
+  const bool paged = a.c.table != nullptr;
+  const uint64_t rows = paged ? uint64_t(kBlock) : uint64_t(a.max_seq_len);
+  const uint64_t depth = paged ? uint64_t(a.c.n_pages) * a.c.hkv : uint64_t(a.batch) * a.c.hkv;
+  const uint64_t depth_bytes = (paged ? uint64_t(kBlock) : uint64_t(a.c.cap)) * D * 2;
+  cudaError_t e = make_bf16_tensor_map_3d_sw128(&kmap, a.c.k, D, rows, depth, depth_bytes, kBlock);
+  if (e == cudaSuccess)
+    e = make_bf16_tensor_map_3d_sw128(&vmap, a.c.v, D, rows, depth, depth_bytes, kBlock);
+  if (e == cudaSuccess)
+    e = make_bf16_tensor_map_3d_sw128_box(&qmap, a.q, D, uint64_t(a.hq), uint64_t(a.n_tokens),
+                                          uint64_t(D) * 2, uint64_t(a.hq) * D * 2, group,
+                                          kTileRows / group);
+  if (e != cudaSuccess) return e;
+  auto kern = paged ? prompt_kernel<D, true> : prompt_kernel<D, false>;
+  e = set_smem_attrs(kern, T::kDynSmem);
+  if (e != cudaSuccess) return e;
+  const int ctas = prompt_ctas(a.n_tokens, a.batch, a.c.hkv, group, a.max_seq_len);
+  e = launch_pdl(kern, dim3(ctas), dim3(kThreads), T::kDynSmem, stream, kmap, vmap, qmap, a);
+  if (e != cudaSuccess || a.max_seq_len <= kWholeTokens) return e;
+  return launch_pdl(prompt_merge_kernel<D>, dim3(ctas, D / kMergeDims), dim3(kUnitRows), 0,
+                    stream, a, ctas);
 }
 
 }  // namespace
 
-size_t prompt_partial_bytes(const cobs_dims*, int64_t, int64_t) { return 0; }
+size_t prompt_partial_bytes(const cobs_dims* d, int64_t n_tokens, int64_t max_seq_len) {
+  if (n_tokens == 0 || max_seq_len <= kWholeTokens) return 0;
+  const int ctas = prompt_ctas(n_tokens, d->batch, d->num_kv_heads,
+                               d->num_q_heads / d->num_kv_heads, max_seq_len);
+  return kMaxCtas * 2 * sizeof(SlotNote) + size_t(ctas) * 2 * slot_floats(d->head_dim) * 4;
+}
 
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream) {
-  const int64_t ctas = (a.n_tokens * a.hq + kPromptWarps - 1) / kPromptWarps;
-  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  auto kern = a.d == 128 ? prompt_rows_kernel<128> : prompt_rows_kernel<64>;
-  return launch_pdl(kern, dim3(unsigned(ctas)), dim3(32 * kPromptWarps), 0, stream, a);
+  return a.d == 128 ? launch_d<128>(a, stream) : launch_d<64>(a, stream);
 }
 
 }  // namespace cobs
