@@ -41,6 +41,29 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
   return lo;
 }
 
+// Bounded mbarrier wait like wait_or_abort, for waits on the critical path:
+// the clock is first read after 64 tries (reading the global timer on every
+// wait that does not succeed at once adds its latency to each step of a
+// pipeline).
+__device__ __forceinline__ bool wait_step(uint64_t* bar, uint32_t parity, int32_t* status,
+                                          volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        report(status, COBS_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 // Two fp32 -> packed bf16 (low half: x), nearest even, NaN kept.
 __device__ __forceinline__ uint32_t bf16x2_bits(float x, float y) {
   uint32_t r;

@@ -49,7 +49,8 @@ constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kSoftRegs = 208, kOtherRegs = 80;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "register split");
 constexpr int kTileRows = 128;
-constexpr int kKeys = 128;               // keys per iteration
+constexpr int kKeyShift = 7;
+constexpr int kKeys = 1 << kKeyShift;    // keys per iteration
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kMaxCtas = 148;            // one per SM
 constexpr int64_t kWholeTokens = 1024;   // longest sequence whose units are never cut
@@ -57,6 +58,7 @@ constexpr int kMinShare = 4;             // iterations of a share, at least
 constexpr int kSegQ = 2;                 // segments handed from the producer to the others
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kTmemCols = 512;      // S0, S1 (P over them), O0, O1
+constexpr int kPolyOfFour = 1;           // of four pairs of weights, those by exp2_poly
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D>
@@ -91,28 +93,23 @@ struct SlotNote {
   int32_t type, pad;
 };
 
-__host__ __device__ inline int64_t floor_div(int64_t a, int64_t b) {
-  const int64_t q = a / b;
-  return a % b != 0 && (a < 0) != (b < 0) ? q - 1 : q;
-}
-__host__ __device__ inline int64_t div_up(int64_t a, int64_t b) { return -floor_div(-a, b); }
-
 // Units of one sequence and kv-head: count rows at positions [len - count,
-// len), `k` tokens per unit.  A unit's iterations cover the keys up to its
-// last position, one iteration at least (rows before the sequence's start
-// have no key and still need their outputs).
+// len), 2^ks tokens per unit (2^ks = 256 / G).  A unit's iterations cover the
+// keys up to its last position, one iteration at least (rows before the
+// sequence's start have no key and still need their outputs).
 struct SeqUnits {
   int64_t c, count, len;   // c = len - count
-  int32_t k;
-  __host__ __device__ int64_t units() const { return (count + k - 1) / k; }
+  int32_t ks;
+  __host__ __device__ int64_t units() const { return (count + (int64_t(1) << ks) - 1) >> ks; }
   __host__ __device__ int64_t iters(int64_t u) const {
-    const int64_t end = c + (u + 1) * k < len ? c + (u + 1) * k : len;
-    const int64_t n = div_up(end, kKeys);
+    const int64_t e = c + ((u + 1) << ks), end = e < len ? e : len;
+    const int64_t n = (end + kKeys - 1) >> kKeyShift;
     return n > 1 ? n : 1;
   }
   // Iterations of the first n units.  For a full unit j = u + 1 they are
-  // max(1, ceil((c + k j) / 128)); with k = 128 / m this is ceil((c' + j) / m),
-  // c' = ceil(c / k), and with k = 128 s it is ceil(c / 128) + s j.
+  // max(1, ceil((c + k j) / 128)), k = 2^ks; with k = 128 / m this is
+  // ceil((c' + j) / m), c' = ceil(c / k), and with k = 128 s it is
+  // ceil(c / 128) + s j.
   __host__ __device__ int64_t before(int64_t n) const {
     int64_t extra = 0;
     if (n > 0 && n == units()) {   // the last unit may be short
@@ -120,29 +117,31 @@ struct SeqUnits {
       extra = iters(n);
     }
     if (n <= 0) return extra;
-    if (k < kKeys) {
-      const int64_t m = kKeys / k, cp = div_up(c, k);
-      int64_t n0 = -cp < 0 ? 0 : (-cp > n ? n : -cp);   // units with no key: 1 each
-      auto f = [m](int64_t x) {   // sum of ceil(y / m) over y = 1 .. x
-        const int64_t q = x / m, r = x % m;
-        return m * (q * (q + 1) / 2) + r * (q + 1);
+    if (ks < kKeyShift) {
+      const int ms = kKeyShift - ks;
+      const int64_t cp = (c + (int64_t(1) << ks) - 1) >> ks;
+      const int64_t n0 = -cp < 0 ? 0 : (-cp > n ? n : -cp);   // units with no key: 1 each
+      auto f = [ms](int64_t x) {   // sum of ceil(y / m) over y = 1 .. x
+        const int64_t q = x >> ms, r = x - (q << ms);
+        return ((q * (q + 1) >> 1) << ms) + r * (q + 1);
       };
       if (n0 == n) return extra + n;
       return extra + n0 + f(cp + n) - f(cp > 0 ? cp : 0);
     }
-    const int64_t s = k / kKeys, cp = div_up(c, kKeys);
-    int64_t n0 = floor_div(-cp, s);
+    const int ss = ks - kKeyShift;
+    const int64_t cp = (c + kKeys - 1) >> kKeyShift;
+    int64_t n0 = -cp >> ss;
     n0 = n0 < 0 ? 0 : (n0 > n ? n : n0);
-    return extra + n0 + (n - n0) * cp + s * (n * (n + 1) - n0 * (n0 + 1)) / 2;
+    return extra + n0 + (n - n0) * cp + ((n * (n + 1) - n0 * (n0 + 1)) >> 1 << ss);
   }
   // Shares are counted in units (whole) or in iterations.
   __host__ __device__ int64_t weight(bool whole) const { return whole ? units() : before(units()); }
 };
 
-__device__ __forceinline__ SeqUnits seq_units(const PromptArgs& a, int64_t b, int k,
+__device__ __forceinline__ SeqUnits seq_units(const PromptArgs& a, int64_t b, int ks,
                                               bool reporter) {
   SeqUnits s;
-  s.k = k;
+  s.ks = ks;
   s.count = a.cu != nullptr ? int64_t(__ldg(a.cu + b + 1)) - __ldg(a.cu + b) : 1;
   if (s.count < 0) s.count = 0;
   s.len = __ldg(a.seq_lens + b);
@@ -154,14 +153,121 @@ __device__ __forceinline__ SeqUnits seq_units(const PromptArgs& a, int64_t b, in
   return s;
 }
 
-// D[tmem] (+)= A[tmem] B: A is bf16, two per column.
-__device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+// A CTA's share of the work: where it starts and how much it is (units when
+// `whole`, else iterations).
+struct Share {
+  int64_t left;
+  int32_t b, h, u, it;
+};
+
+// The share of CTA blockIdx.x; whole warp.
+__device__ __forceinline__ Share find_share(const PromptArgs& a, int lane) {
+  const bool whole = a.max_seq_len <= kWholeTokens;
+  const int hkv = a.c.hkv;
+  const int ks = 8 - __ffs(a.hq / hkv) + 1;
+  int64_t total = 0;
+  for (int64_t b = lane; b < a.batch; b += 32)
+    total += seq_units(a, b, ks, blockIdx.x == 0).weight(whole);
+  total = warp_sum64(total) * hkv;
+  int64_t n = whole ? total : total / kMinShare;
+  n = n < 1 ? 1 : (n > int64_t(gridDim.x) ? int64_t(gridDim.x) : n);
+  Share s{};
+  if (int64_t(blockIdx.x) >= n) return s;
+  const int64_t t0 = total * int64_t(blockIdx.x) / n;
+  s.left = total * (int64_t(blockIdx.x) + 1) / n - t0;
+  int64_t skipped = 0, w_b = 0;
+  for (int64_t b0 = 0; b0 < a.batch && s.left > 0; b0 += 32) {
+    const int64_t mine = b0 + lane < a.batch ? b0 + lane : a.batch - 1;
+    const int64_t wgt =
+        b0 + lane < a.batch ? seq_units(a, mine, ks, false).weight(whole) * hkv : 0;
+    int64_t inc = wgt;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, m);
+      if (lane >= m) inc += up;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, skipped + inc > t0);
+    if (past != 0) {
+      const int l = __ffs(past) - 1;
+      s.b = int32_t(b0 + l);
+      w_b = __shfl_sync(0xffffffffu, wgt, l);
+      skipped += __shfl_sync(0xffffffffu, inc - wgt, l);
+      break;
+    }
+    skipped += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (s.left > 0) {
+    const SeqUnits su = seq_units(a, s.b, ks, false);
+    const int64_t w_h = w_b / hkv;
+    s.h = int32_t((t0 - skipped) / w_h);
+    const int64_t rest = (t0 - skipped) % w_h;
+    if (whole) {
+      s.u = int32_t(rest);
+    } else {
+      int64_t lo = 0, hi = su.units() - 1;   // the last u with before(u) <= rest
+      while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (su.before(mid) <= rest) lo = mid;
+        else hi = mid - 1;
+      }
+      s.u = int32_t(lo);
+      s.it = int32_t(rest - su.before(lo));
+    }
+  }
+  return s;
+}
+
+// The products are issued by one elected thread of a warp whose lanes all run
+// the same code: operands that the compiler can see to be the same in every
+// lane stay in uniform registers.  (Issued from a branch that one lane takes,
+// each product cost about 100 cycles of moving its operands there, more than
+// the 64 that the tensor core needs for it.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
+}
+// D[tmem] (+)= A B, both in shared memory.
+__device__ __forceinline__ void umma_bf16_if(uint32_t elected, uint32_t tmem_d, uint64_t adesc,
+                                             uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B: A is bf16, two per column.
+__device__ __forceinline__ void umma_bf16_ta_if(uint32_t elected, uint32_t tmem_d,
+                                                uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(elected)
       : "memory");
 }
 
@@ -179,20 +285,52 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* v) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of a pair on the fused multiply-add pipe, x <= 9, below -126 taken as
+// -126: x = n + r with n = round(x) from the low bits of x + 1.5 2^23 and
+// |r| <= 1/2, 2^r by the cubic whose relative error is smallest on that
+// interval (equal-ripple fit, 7.5e-5 = 2^-13.7; a weight is rounded to bf16,
+// 2^-8, afterwards), n added to the exponent bits.
+__device__ __forceinline__ float2 exp2_poly(uint64_t x2) {
+  float2 x = unpack2(x2);
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  x2 = pack2(x);
+  auto both = [](float v) { return pack2(make_float2(v, v)); };
+  const uint64_t t = add2(x2, both(12582912.f));
+  const uint64_t r = fma2(add2(t, both(-12582912.f)), both(-1.f), x2);
+  uint64_t y = fma2(both(0.0551716685f), r, both(0.242611125f));
+  y = fma2(y, r, both(0.693260968f));
+  y = fma2(y, r, both(0.999928057f));
+  const float2 tv = unpack2(t), yv = unpack2(y);
+  return make_float2(
+      __uint_as_float((__float_as_uint(tv.x) << 23) + __float_as_uint(yv.x)),
+      __uint_as_float((__float_as_uint(tv.y) << 23) + __float_as_uint(yv.y)));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -201,11 +339,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  return v;
-}
+template <int I>
+struct Index {
+  static constexpr int value = I;
+};
+
 
 constexpr size_t slot_floats(int d) { return size_t(kUnitRows) * (d + 2); }
 
@@ -221,7 +359,7 @@ __device__ __forceinline__ SlotNote* slot_note(const PromptArgs& a, int64_t slot
 // Wait of a whole warp; false (for every lane) when it ran out.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status,
                                           volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, status, abort_flag));
+  return __all_sync(0xffffffffu, wait_step(bar, parity, status, abort_flag));
 }
 
 template <int D, bool kPaged>
@@ -241,8 +379,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   __shared__ Segment seg_q[kSegQ];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_s;
+  __shared__ Share share;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane
   const int group = a.hq / a.c.hkv;
   const int tt = kTileRows / group;        // tokens of a tile
 
@@ -272,6 +412,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
   if (warp == 0) tmem_alloc(&tmem_slot, kTmemCols);
   pdl_wait();
+  if (warp == kProducerWarp) {
+    const Share s = find_share(a, lane);
+    if (lane == 0) share = s;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -283,78 +427,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (warp == kProducerWarp) {
     // ==================== schedule and TMA (whole warp) ====================
     const bool whole = a.max_seq_len <= kWholeTokens;
+    const int ks = 8 - __ffs(group) + 1;      // tokens of a unit: 256 / G = 2^ks
     const int k_unit = 2 * tt;
     const int hkv = a.c.hkv;
-    // this CTA's share [t0, t1) of the work
-    int64_t total = 0;
-    for (int64_t b = lane; b < a.batch; b += 32)
-      total += seq_units(a, b, k_unit, blockIdx.x == 0).weight(whole);
-    total = warp_sum64(total) * hkv;
-    int64_t n = whole ? total : total / kMinShare;
-    n = n < 1 ? 1 : (n > int64_t(gridDim.x) ? int64_t(gridDim.x) : n);
-    int64_t t0 = 0, t1 = 0;
-    if (int64_t(blockIdx.x) < n) {
-      t0 = total * int64_t(blockIdx.x) / n;
-      t1 = total * (int64_t(blockIdx.x) + 1) / n;
-    }
-    // the sequence, kv-head and unit of t0
-    int64_t b = 0, skipped = 0, w_b = 0;
-    SeqUnits su{};
-    for (int64_t b0 = 0; b0 < a.batch && t0 < t1; b0 += 32) {
-      const int64_t mine = b0 + lane < a.batch ? b0 + lane : a.batch - 1;
-      const int64_t wgt =
-          b0 + lane < a.batch ? seq_units(a, mine, k_unit, false).weight(whole) * hkv : 0;
-      int64_t inc = wgt;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, inc, m);
-        if (lane >= m) inc += up;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, skipped + inc > t0);
-      if (past != 0) {
-        const int l = __ffs(past) - 1;
-        b = b0 + l;
-        w_b = __shfl_sync(0xffffffffu, wgt, l);
-        skipped += __shfl_sync(0xffffffffu, inc - wgt, l);
-        break;
-      }
-      skipped += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    int64_t h = 0, u = 0, it = 0;
-    if (t0 < t1) {
-      su = seq_units(a, b, k_unit, false);
-      const int64_t w_h = w_b / hkv;
-      h = (t0 - skipped) / w_h;
-      const int64_t rest = (t0 - skipped) % w_h;
-      if (whole) {
-        u = rest;
-      } else {
-        int64_t lo = 0, hi = su.units() - 1;   // the last u with before(u) <= rest
-        while (lo < hi) {
-          const int64_t mid = (lo + hi + 1) / 2;
-          if (su.before(mid) <= rest) lo = mid;
-          else hi = mid - 1;
-        }
-        u = lo;
-        it = rest - su.before(u);
-      }
-    }
+    int64_t left = share.left;
+    int32_t b = share.b, h = share.h, u = share.u, it = share.it;
+    SeqUnits su = seq_units(a, b, ks, false);
     uint32_t item = 0;       // ring items issued
     uint32_t tails = 0;      // uses of v_tail
     uint32_t nseg = 0;
     SlotNote note[2] = {};
     bool ok = true;
-    int64_t left = t1 - t0;
     while (left > 0 && ok) {
       const int64_t n_it = su.iters(u);
       Segment g;
-      g.b = int32_t(b);
-      g.h = int32_t(h);
-      g.tok0 = (a.cu != nullptr ? int64_t(__ldg(a.cu + b)) : b) + u * k_unit;
-      g.pos0 = su.c + u * k_unit;
+      g.b = b;
+      g.h = h;
+      g.tok0 = (a.cu != nullptr ? int64_t(__ldg(a.cu + b)) : int64_t(b)) + int64_t(u) * k_unit;
+      g.pos0 = su.c + int64_t(u) * k_unit;
       g.len = su.len;
-      g.ntok = int32_t(su.count - u * k_unit < k_unit ? su.count - u * k_unit : k_unit);
-      g.it0 = int32_t(it);
+      const int64_t rest = su.count - int64_t(u) * k_unit;
+      g.ntok = int32_t(rest < k_unit ? rest : k_unit);
+      g.it0 = it;
       g.it1 = int32_t(whole || n_it - it <= left ? n_it : it + left);
       const bool first = g.it0 == 0, last = g.it1 == n_it;
       g.type = first ? (last ? kWhole : kBegin) : (last ? kEnd : kMiddle);
@@ -401,7 +495,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             if (j >= pg0 + 32 || j < pg0) {
               pg0 = j;
               const int64_t jj = j + lane;
-              page = jj < blocks ? __ldg(a.c.table + b * a.c.table_stride + jj) : -1;
+              page = jj < blocks ? __ldg(a.c.table + int64_t(b) * a.c.table_stride + jj) : -1;
             }
             const int32_t p = __shfl_sync(0xffffffffu, page, int(j - pg0));
             const bool good = p >= 0 && p < a.c.n_pages;
@@ -464,7 +558,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           h = 0;
           do {
             ++b;
-            if (b < a.batch) su = seq_units(a, b, k_unit, false);
+            if (b < a.batch) su = seq_units(a, b, ks, false);
           } while (b < a.batch && su.count == 0);
           if (b >= a.batch) left = 0;
         }
@@ -490,91 +584,96 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       (void)mbar_wait_bounded(&full[x % kStages], (x / kStages) & 1, a.status);
   } else if (warp == kMmaWarp) {
     // ============================= products ================================
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = umma_idesc_bf16(128, kKeys);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
-      const uint32_t q0 = smem_addr(base + T::kOffQ);
-      uint32_t item = 0, nseg = 0;
-      uint32_t np[2] = {0, 0};     // P tiles consumed
-      bool ok = true, issued = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wait_or_abort(bar, parity, a.status, &abort_s);
-      };
-      // (a descriptor's address field counts 16 bytes; shared memory ends
-      // below 2^18, so adding to it never carries out of its 14 bits)
-      auto qk = [&](int w, uint32_t st) {
-        const uint64_t qd = umma_desc_sw128(q0 + w * T::kBytes);
-        const uint64_t kd = umma_desc_sw128(smem_addr(base + st * T::kBytes));
+    constexpr uint32_t idesc_qk = umma_idesc_bf16(128, kKeys);
+    constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
+    const uint32_t elected = elect_one();
+    const uint32_t ring0 = smem_addr(base), q0 = ring0 + T::kOffQ;
+    uint32_t item = 0, nseg = 0;
+    uint32_t np0 = 0, np1 = 0;   // P tiles consumed
+    bool ok = true, issued = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return warp_wait(bar, parity, a.status, &abort_s);
+    };
+    // (a descriptor's address field counts 16 bytes; shared memory ends
+    // below 2^18, so adding to it never carries out of its 14 bits)
+    auto qk = [&](auto wc, uint32_t st) {
+      constexpr int w = decltype(wc)::value;
+      const uint64_t qd = umma_desc_sw128(q0 + w * T::kBytes);
+      const uint64_t kd = umma_desc_sw128(ring0 + st * T::kBytes);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * T::kSlabBytes + (ks & 3) * 32) >> 4;
-          umma_bf16(tmem + 128u * w, qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[w]);
-        issued = true;
-      };
-      while (ok) {
-        const int qs = nseg % kSegQ;
-        if (!wait(&seg_full[qs], (nseg / kSegQ) & 1)) break;
-        const int type = seg_q[qs].type, ntok = seg_q[qs].ntok;
-        const int n_it = seg_q[qs].it1 - seg_q[qs].it0;
-        mbar_arrive(&seg_empty[qs]);
-        if (type == kNone) break;
-        const int tiles = ntok > tt ? 2 : 1;
-        uint32_t kst = item % kStages;
-        if (!wait(&q_full, nseg & 1) || !wait(&full[kst], (item / kStages) & 1)) break;
-        ++nseg;
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = ((ks >> 2) * T::kSlabBytes + (ks & 3) * 32) >> 4;
+        umma_bf16_if(elected, tmem + 128u * w, qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+      }
+      umma_commit_if(elected, &s_full[w]);
+      issued = true;
+    };
+    auto pv = [&](auto wc, uint32_t st, uint32_t accumulate) {
+      constexpr int w = decltype(wc)::value;
+      const uint64_t vd = umma_desc_sw128_mn(ring0 + st * T::kBytes, T::kSlabBytes);
+#pragma unroll
+      for (int ks = 0; ks < kKeys / 16; ++ks)
+        umma_bf16_ta_if(elected, tmem + 256u + uint32_t(D) * w, tmem + 128u * w + 8u * ks,
+                        vd + ks * (2048 >> 4), idesc_pv, ks > 0 ? 1u : accumulate);
+    };
+    const Index<0> tile0;
+    const Index<1> tile1;
+    while (ok) {
+      const int qs = nseg % kSegQ;
+      if (!wait(&seg_full[qs], (nseg / kSegQ) & 1)) break;
+      const int type = __shfl_sync(0xffffffffu, seg_q[qs].type, 0);
+      const int ntok = __shfl_sync(0xffffffffu, seg_q[qs].ntok, 0);
+      const int n_it = __shfl_sync(0xffffffffu, seg_q[qs].it1 - seg_q[qs].it0, 0);
+      if (lane == 0) mbar_arrive(&seg_empty[qs]);
+      __syncwarp();
+      if (type == kNone) break;
+      const bool two = ntok > tt;
+      uint32_t kst = item % kStages;
+      if (!wait(&q_full, nseg & 1) || !wait(&full[kst], (item / kStages) & 1)) break;
+      ++nseg;
+      tc_fence_after();
+      qk(tile0, kst);
+      if (two) qk(tile1, kst);
+      umma_commit_if(elected, &empty[kst]);
+      if (n_it == 1) umma_commit_if(elected, &q_empty);
+      for (int i = 0; i < n_it; ++i) {
+        const uint32_t vi = item + 1, vst = vi % kStages;
+        const bool more = i + 1 < n_it;
+        item += 2;
+        kst = item % kStages;
+        ok = wait(&full[vst], (vi / kStages) & 1) && wait(&p_full[0], np0 & 1);
+        if (!ok) break;
+        ++np0;
         tc_fence_after();
-#pragma unroll 1
-        for (int w = 0; w < tiles; ++w) qk(w, kst);
-        umma_commit(&empty[kst]);
-        if (n_it == 1) umma_commit(&q_empty);
-        for (int i = 0; i < n_it && ok; ++i) {
-          const uint32_t vi = item + 1, vst = vi % kStages;
-          item += 2;
-          kst = item % kStages;
-          if (!wait(&full[vst], (vi / kStages) & 1)) {
-            ok = false;
-            break;
-          }
-#pragma unroll 1
-          for (int w = 0; w < tiles; ++w) {
-            if (!wait(&p_full[w], np[w] & 1)) {
-              ok = false;
-              break;
-            }
-            ++np[w];
-            tc_fence_after();
-            const uint64_t vd =
-                umma_desc_sw128_mn(smem_addr(base + vst * T::kBytes), T::kSlabBytes);
-#pragma unroll
-            for (int ks = 0; ks < kKeys / 16; ++ks)
-              umma_bf16_ta(tmem + 256u + uint32_t(D) * w, tmem + 128u * w + 8u * ks,
-                           vd + ks * (2048 >> 4), idesc_pv, (i > 0 || ks > 0) ? 1u : 0u);
-            if (w == tiles - 1) umma_commit(&empty[vst]);
-            if (i + 1 == n_it) {
-              umma_commit(&o_full[w]);
-              continue;
-            }
-            if (w == 0) {
-              if (!wait(&full[kst], (item / kStages) & 1)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-            }
-            qk(w, kst);
-          }
-          if (ok && i + 1 < n_it) {
-            umma_commit(&empty[kst]);
-            if (i + 2 == n_it) umma_commit(&q_empty);
-          }
+        pv(tile0, vst, i > 0 ? 1u : 0u);
+        if (!two) umma_commit_if(elected, &empty[vst]);
+        if (more) {
+          ok = wait(&full[kst], (item / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          qk(tile0, kst);
+        } else {
+          umma_commit_if(elected, &o_full[0]);
+        }
+        if (two) {
+          ok = wait(&p_full[1], np1 & 1);
+          if (!ok) break;
+          ++np1;
+          tc_fence_after();
+          pv(tile1, vst, i > 0 ? 1u : 0u);
+          umma_commit_if(elected, &empty[vst]);
+          if (more) qk(tile1, kst);
+          else umma_commit_if(elected, &o_full[1]);
+        }
+        if (more) {
+          umma_commit_if(elected, &empty[kst]);
+          if (i + 2 == n_it) umma_commit_if(elected, &q_empty);
         }
       }
-      if (issued) {   // every product must be complete before TMEM is freed
-        umma_commit(&drain);
-        (void)mbar_wait_bounded(&drain, 0, a.status);
-      }
+    }
+    if (issued) {   // every product must be complete before TMEM is freed
+      umma_commit_if(elected, &drain);
+      (void)mbar_wait_bounded(&drain, 0, a.status);
     }
     __syncwarp();
   }
@@ -622,26 +721,36 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (busy) {
           tc_fence_after();
           float s[kKeys];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_addr + 32u * c, s + 32 * c);
+          tmem_ld32_nowait(s_addr, s);
+          tmem_ld32_nowait(s_addr + 32u, s + 32);
           tmem_wait_ld();
-          if (key0 + kKeys - 1 > pos_w || (kPaged && gone != 0)) {
-            const int64_t room = pos - key0;
-            const int lim = room > kKeys ? kKeys : (room < -1 ? -1 : int(room));
+          tmem_ld32_nowait(s_addr + 64u, s + 64);
+          tmem_ld32_nowait(s_addr + 96u, s + 96);
+          // the maximum of the first half while the second comes in
+          const bool masked = key0 + kKeys - 1 > pos_w || (kPaged && gone != 0);
+          const int64_t room = pos - key0;
+          const int lim = room > kKeys ? kKeys : (room < -1 ? -1 : int(room));
+          auto hide = [&](int c0) {
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c) {
-              const bool hide = c > lim || (kPaged && ((gone >> (c >> 6)) & 1u));
-              s[c] = hide ? -INFINITY : s[c];
-            }
-          }
+            for (int c = c0; c < c0 + 64; ++c)
+              if (c > lim || (kPaged && ((gone >> (c >> 6)) & 1u))) s[c] = -INFINITY;
+          };
+          if (masked) hide(0);
           float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
 #pragma unroll
-          for (int c = 4; c < kKeys; c += 4) {
+          for (int c = 4; c < 64; c += 4) {
+            mx0 = max3(mx0, s[c], s[c + 1]);
+            mx1 = max3(mx1, s[c + 2], s[c + 3]);
+          }
+          tmem_wait_ld();
+          if (masked) hide(64);
+#pragma unroll
+          for (int c = 64; c < kKeys; c += 4) {
             mx0 = max3(mx0, s[c], s[c + 1]);
             mx1 = max3(mx1, s[c + 2], s[c + 3]);
           }
           const float mx = fmaxf(mx0, mx1) * a.scale_log2;
-          const bool raise = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
+          const bool raise = mx > m + kRescaleLog2;   // also the first key of a row
           if (__any_sync(0xffffffffu, raise)) {
             const float mn = raise ? mx : m;
             const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
@@ -649,29 +758,42 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             l *= alpha;
             if (i > g.it0) {
 #pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(o_addr + c, o);
+              for (int c = 0; c < D; c += 16) {   // narrow: 128 scores are live
+                float o[16];
+                tmem_ld16(o_addr + c, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                tmem_st32(o_addr + c, reinterpret_cast<const uint32_t*>(o));
+                for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                tmem_st16(o_addr + c, reinterpret_cast<const uint32_t*>(o));
               }
             }
           }
           const float neg_m = m == -INFINITY ? 0.f : -m;
-          float sum0 = 0.f, sum1 = 0.f;
-          uint32_t p[kKeys / 2];
+          const uint64_t scale2 = pack2(make_float2(a.scale_log2, a.scale_log2));
+          const uint64_t neg_m2 = pack2(make_float2(neg_m, neg_m));
+          uint64_t sum_a = 0, sum_b = 0;
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 2) {
-            const float p0 = hw_exp2(fmaf(s[c], a.scale_log2, neg_m));
-            const float p1 = hw_exp2(fmaf(s[c + 1], a.scale_log2, neg_m));
-            sum0 += p0;
-            sum1 += p1;
-            p[c / 2] = bf16x2_bits(p0, p1);
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              uint64_t x = fma2(pack2(make_float2(s[c + 2 * e], s[c + 2 * e + 1])), scale2, neg_m2);
+              float2 pe;
+              if (e % 4 < kPolyOfFour) {
+                pe = exp2_poly(x);
+              } else {
+                const float2 xv = unpack2(x);
+                pe = make_float2(hw_exp2(xv.x), hw_exp2(xv.y));
+              }
+              if (e & 1) sum_b = add2(sum_b, pack2(pe));
+              else sum_a = add2(sum_a, pack2(pe));
+              p[e] = bf16x2_bits(pe.x, pe.y);
+            }
+            tmem_st16(s_addr + uint32_t(c / 2), p);
           }
-          l += sum0 + sum1;
-          tmem_st32(s_addr, p);
-          tmem_st32(s_addr + 32u, p + 32);
+          {
+            const float2 t = unpack2(add2(sum_a, sum_b));
+            l += t.x + t.y;
+          }
           tmem_wait_st();
           tc_fence_before();
         }
@@ -687,7 +809,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const bool mine = tok < g.ntok;
         if (g.type == kWhole) {
           const int64_t r = (g.tok0 + tok) * a.hq + g.h * group + row % group;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const bool some = m != -INFINITY;           // the row has a key
+          const float inv = some ? 1.f / l : 0.f;
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -699,14 +822,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 uint32_t v[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                  v[x] = l > 0.f ? bf16x2_bits(o[8 * e + 2 * x] * inv, o[8 * e + 2 * x + 1] * inv)
+                  v[x] = some ? bf16x2_bits(o[8 * e + 2 * x] * inv, o[8 * e + 2 * x + 1] * inv)
                                  : 0u;
                 dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
               }
             }
           }
           if (mine && a.lse != nullptr)
-            a.lse[r] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            a.lse[r] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
         } else {
           float* part = slot_rows(a, D, 2 * int64_t(blockIdx.x) + (g.type == kBegin ? 1 : 0));
           const int r = w * kTileRows + row;
@@ -779,7 +902,7 @@ __global__ void __launch_bounds__(kUnitRows) prompt_merge_kernel(const PromptArg
     M = mn;
   }
   const int64_t row = (g.tok0 + tok) * a.hq + g.h * group + r % group;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = M != -INFINITY ? 1.f / L : 0.f;
   uint32_t out[kMergeDims / 2];
 #pragma unroll
   for (int e = 0; e < kMergeDims / 2; ++e) out[e] = bf16x2_bits(o[2 * e] * inv, o[2 * e + 1] * inv);
@@ -788,7 +911,7 @@ __global__ void __launch_bounds__(kUnitRows) prompt_merge_kernel(const PromptArg
     reinterpret_cast<uint4*>(a.out + row * D + d0)[e] =
         make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
   if (blockIdx.y == 0 && a.lse != nullptr)
-    a.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    a.lse[row] = M != -INFINITY ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 // CTAs of a launch: no more than there can be shares.
