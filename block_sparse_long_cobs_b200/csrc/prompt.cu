@@ -42,18 +42,20 @@
 namespace cobs {
 namespace {
 
-constexpr int kThreads = 384;            // two softmax warpgroups, one for the rest
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
-// Registers: 384 x 168 at launch, of which the softmax threads (a row of 128
-// scores each) take 208 and the others keep 80.
-constexpr int kSoftRegs = 208, kOtherRegs = 80;
-static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "register split");
+constexpr int kThreads = 640;            // four softmax warpgroups, one for the rest
+constexpr int kSoftWarps = 16;
+constexpr int kProducerWarp = 16, kMmaWarp = 17;
+// Registers: 640 x 96 at launch, of which the softmax threads (half a row of
+// scores each) take 104 and the others keep 64.
+constexpr int kSoftRegs = 104, kOtherRegs = 64;
+static_assert(512 * kSoftRegs + 128 * kOtherRegs <= 640 * 96, "register split");
 constexpr int kTileRows = 128;
 constexpr int kKeyShift = 7;
 constexpr int kKeys = 1 << kKeyShift;    // keys per iteration
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kMaxCtas = 148;            // one per SM
 constexpr int64_t kWholeTokens = 1024;   // longest sequence whose units are never cut
+constexpr int kUnitCost = 2;             // what starting and ending a unit costs, in iterations
 constexpr int kMinShare = 4;             // iterations of a share, at least
 constexpr int kSegQ = 2;                 // segments handed from the producer to the others
 constexpr float kRescaleLog2 = 8.f;
@@ -66,7 +68,7 @@ struct Tile {
   static constexpr int kSlabs = D / 64;
   static constexpr int kSlabBytes = 128 * 128;          // 128 rows x 64 columns bf16
   static constexpr int kBytes = kSlabs * kSlabBytes;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kOffQ = kStages * kBytes;
   static constexpr int kDynSmem = kOffQ + 2 * kBytes + 1024;
 };
@@ -134,8 +136,10 @@ struct SeqUnits {
     n0 = n0 < 0 ? 0 : (n0 > n ? n : n0);
     return extra + n0 + (n - n0) * cp + ((n * (n + 1) - n0 * (n0 + 1)) >> 1 << ss);
   }
-  // Shares are counted in units (whole) or in iterations.
-  __host__ __device__ int64_t weight(bool whole) const { return whole ? units() : before(units()); }
+  // Shares are counted in units (whole) or in iterations, with kUnitCost more
+  // for the end of each unit.
+  __host__ __device__ int64_t cost(int64_t n) const { return before(n) + kUnitCost * n; }
+  __host__ __device__ int64_t weight(bool whole) const { return whole ? units() : cost(units()); }
 };
 
 __device__ __forceinline__ SeqUnits seq_units(const PromptArgs& a, int64_t b, int ks,
@@ -210,14 +214,14 @@ __device__ __forceinline__ Share find_share(const PromptArgs& a, int lane) {
     if (whole) {
       s.u = int32_t(rest);
     } else {
-      int64_t lo = 0, hi = su.units() - 1;   // the last u with before(u) <= rest
+      int64_t lo = 0, hi = su.units() - 1;   // the last u with cost(u) <= rest
       while (lo < hi) {
         const int64_t mid = (lo + hi + 1) / 2;
-        if (su.before(mid) <= rest) lo = mid;
+        if (su.cost(mid) <= rest) lo = mid;
         else hi = mid - 1;
       }
       s.u = int32_t(lo);
-      s.it = int32_t(rest - su.before(lo));
+      s.it = int32_t(rest - su.cost(lo));
     }
   }
   return s;
@@ -380,6 +384,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_s;
   __shared__ Share share;
+  __shared__ float half_row[2][2][kTileRows];   // a tile's row over half its keys: max, sum
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane
@@ -400,12 +405,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     mbar_init(&drain, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 4);
+      mbar_init(&p_full[w], 8);
       mbar_init(&o_full[w], 1);
     }
     for (int s = 0; s < kSegQ; ++s) {
       mbar_init(&seg_full[s], 1);
-      mbar_init(&seg_empty[s], 9);
+      mbar_init(&seg_empty[s], kSoftWarps + 1);
     }
     fence_barrier_init();
     abort_s = 0;
@@ -438,8 +443,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     uint32_t nseg = 0;
     SlotNote note[2] = {};
     bool ok = true;
+    auto next_unit = [&]() {
+      it = 0;
+      if (++u < su.units()) return;
+      u = 0;
+      if (++h < hkv) return;
+      h = 0;
+      do {
+        ++b;
+        if (b < a.batch) su = seq_units(a, b, ks, false);
+      } while (b < a.batch && su.count == 0);
+      if (b >= a.batch) left = 0;
+    };
     while (left > 0 && ok) {
       const int64_t n_it = su.iters(u);
+      if (it >= n_it) {   // the share starts in what the unit's end costs
+        left -= n_it + kUnitCost - it;
+        next_unit();
+        continue;
+      }
       Segment g;
       g.b = b;
       g.h = h;
@@ -459,7 +481,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         nt.h = g.h;
         nt.type = g.type;
       }
-      left -= whole ? 1 : g.it1 - g.it0;
+      left -= whole ? 1 : (last ? n_it + kUnitCost - it : g.it1 - it);
       // ---- hand the segment over ----
       const int qs = nseg % kSegQ;
       if (nseg >= kSegQ &&
@@ -550,19 +572,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
       }
       if (!ok) break;
-      // ---- the next unit ----
-      it = 0;
-      if (g.it1 == n_it && ++u >= su.units()) {
-        u = 0;
-        if (++h >= hkv) {
-          h = 0;
-          do {
-            ++b;
-            if (b < a.batch) su = seq_units(a, b, ks, false);
-          } while (b < a.batch && su.count == 0);
-          if (b >= a.batch) left = 0;
-        }
-      }
+      if (last) next_unit();
     }
     // the end of the work: an empty segment
     if (ok) {
@@ -613,7 +623,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const uint64_t vd = umma_desc_sw128_mn(ring0 + st * T::kBytes, T::kSlabBytes);
 #pragma unroll
       for (int ks = 0; ks < kKeys / 16; ++ks)
-        umma_bf16_ta_if(elected, tmem + 256u + uint32_t(D) * w, tmem + 128u * w + 8u * ks,
+        umma_bf16_ta_if(elected, tmem + 256u + uint32_t(D) * w,
+                        tmem + 128u * w + (ks >> 2) * 64u + (ks & 3) * 8u,
                         vd + ks * (2048 >> 4), idesc_pv, ks > 0 ? 1u : accumulate);
     };
     const Index<0> tile0;
@@ -680,85 +691,84 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ======================= softmax and output ===========================
-    const int w = warp >> 2;
+    const int w = warp >> 3, half = (warp >> 2) & 1;
     const int row = (warp & 3) * 32 + lane;         // of the tile
+    const int pair_bar = 1 + w * 4 + (warp & 3);    // the two warps of these rows
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + 128u * w;
-    const uint32_t o_addr = tmem + lane_base + 256u + uint32_t(D) * w;
+    // this thread's 64 scores; its weights overwrite the first 32 columns
+    const uint32_t s_addr = tmem + lane_base + 128u * w + 64u * half;
+    const uint32_t o_addr = tmem + lane_base + 256u + uint32_t(D) * w + uint32_t(D / 2) * half;
     const int tok = w * tt + row / group;           // token of the unit
     const int tok_w = w * tt + (warp & 3) * 32 / group;   // the warp's first
     uint32_t nseg = 0, ns = 0, no = 0;
     bool ok = true;
     for (; ok; ++nseg) {
       const int qs = nseg % kSegQ;
-      if (!warp_wait(&seg_full[qs], (nseg / kSegQ) & 1, a.status, &abort_s)) break;
-      const Segment g = seg_q[qs];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_empty[qs]);
-      if (g.type == kNone) break;
-      if (w == 1 && g.ntok <= tt) continue;
-      const bool busy = tok_w < g.ntok;             // a row of the warp is a token's
-      const int64_t pos = g.pos0 + tok;
-      const int64_t pos_w = g.pos0 + tok_w;
+      const bool got = warp_wait(&seg_full[qs], (nseg / kSegQ) & 1, a.status, &abort_s);
+      // the two warps of a row go on together or give up together
+      if (named_bar_or(pair_bar, 64, !got)) break;
+      const bool here = w * tt < seg_q[qs].ntok;  // the tile has rows
+      const bool busy = tok_w < seg_q[qs].ntok;   // a row of the warp is a token's
+      if (seg_q[qs].type == kNone) break;
+      if (!here) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[qs]);
+        continue;
+      }
+      const int it0 = seg_q[qs].it0, it1 = seg_q[qs].it1;
+      const int pos = int(seg_q[qs].pos0) + tok;
+      const int blocks = int((seg_q[qs].len + kBlock - 1) / kBlock);
+      const int32_t* table =
+          kPaged ? a.c.table + int64_t(seg_q[qs].b) * a.c.table_stride + half : nullptr;
       float m = -INFINITY, l = 0.f;
-      for (int i = g.it0; i < g.it1; ++i, ++ns) {
-        const int64_t key0 = int64_t(i) * kKeys;
-        // blocks of this iteration without a page (their keys are not there)
-        uint32_t gone = 0;
+      for (int i = it0; i < it1; ++i, ++ns) {
+        // (paged) this half's block has no page: its keys are not there
+        bool gone = false;
         if constexpr (kPaged) {
-          const int64_t j = 2 * int64_t(i) + lane;
-          bool bad = false;
-          if (busy && lane < 2 && j * kBlock < g.len) {
-            const int32_t p = __ldg(a.c.table + int64_t(g.b) * a.c.table_stride + j);
-            bad = p < 0 || p >= a.c.n_pages;
+          if (busy && 2 * i + half < blocks) {
+            const int32_t p = __ldg(table + 2 * i);
+            gone = p < 0 || p >= a.c.n_pages;
           }
-          gone = __ballot_sync(0xffffffffu, bad);
         }
-        if (!warp_wait(&s_full[w], ns & 1, a.status, &abort_s)) {
+        const bool fail = !warp_wait(&s_full[w], ns & 1, a.status, &abort_s);
+        float s[64];
+        float mx = -INFINITY;
+        if (busy && !fail) {
+          tc_fence_after();
+          tmem_ld32_nowait(s_addr, s);
+          tmem_ld32_nowait(s_addr + 32u, s + 32);
+          tmem_wait_ld();
+          // the last key this row sees, among these 64
+          const int lim = gone ? -1 : pos - i * kKeys - 64 * half;
+          if (__any_sync(0xffffffffu, lim < 63)) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = c > lim ? -INFINITY : s[c];
+          }
+          float mx1 = fmaxf(s[2], s[3]);
+          mx = fmaxf(s[0], s[1]);
+#pragma unroll
+          for (int c = 4; c < 64; c += 4) {
+            mx = max3(mx, s[c], s[c + 1]);
+            mx1 = max3(mx1, s[c + 2], s[c + 3]);
+          }
+          mx = fmaxf(mx, mx1);
+          half_row[w][half][row] = mx;
+        }
+        if (named_bar_or(pair_bar, 64, fail)) {
           ok = false;
           break;
         }
         if (busy) {
-          tc_fence_after();
-          float s[kKeys];
-          tmem_ld32_nowait(s_addr, s);
-          tmem_ld32_nowait(s_addr + 32u, s + 32);
-          tmem_wait_ld();
-          tmem_ld32_nowait(s_addr + 64u, s + 64);
-          tmem_ld32_nowait(s_addr + 96u, s + 96);
-          // the maximum of the first half while the second comes in
-          const bool masked = key0 + kKeys - 1 > pos_w || (kPaged && gone != 0);
-          const int64_t room = pos - key0;
-          const int lim = room > kKeys ? kKeys : (room < -1 ? -1 : int(room));
-          auto hide = [&](int c0) {
-#pragma unroll
-            for (int c = c0; c < c0 + 64; ++c)
-              if (c > lim || (kPaged && ((gone >> (c >> 6)) & 1u))) s[c] = -INFINITY;
-          };
-          if (masked) hide(0);
-          float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
-#pragma unroll
-          for (int c = 4; c < 64; c += 4) {
-            mx0 = max3(mx0, s[c], s[c + 1]);
-            mx1 = max3(mx1, s[c + 2], s[c + 3]);
-          }
-          tmem_wait_ld();
-          if (masked) hide(64);
-#pragma unroll
-          for (int c = 64; c < kKeys; c += 4) {
-            mx0 = max3(mx0, s[c], s[c + 1]);
-            mx1 = max3(mx1, s[c + 2], s[c + 3]);
-          }
-          const float mx = fmaxf(mx0, mx1) * a.scale_log2;
+          mx = fmaxf(mx, half_row[w][half ^ 1][row]) * a.scale_log2;
           const bool raise = mx > m + kRescaleLog2;   // also the first key of a row
           if (__any_sync(0xffffffffu, raise)) {
             const float mn = raise ? mx : m;
             const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
             m = mn;
             l *= alpha;
-            if (i > g.it0) {
+            if (i > it0) {
 #pragma unroll
-              for (int c = 0; c < D; c += 16) {   // narrow: 128 scores are live
+              for (int c = 0; c < D / 2; c += 16) {   // narrow: 64 scores are live
                 float o[16];
                 tmem_ld16(o_addr + c, o);
 #pragma unroll
@@ -772,11 +782,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           const uint64_t neg_m2 = pack2(make_float2(neg_m, neg_m));
           uint64_t sum_a = 0, sum_b = 0;
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
+          for (int c = 0; c < 64; c += 32) {
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              uint64_t x = fma2(pack2(make_float2(s[c + 2 * e], s[c + 2 * e + 1])), scale2, neg_m2);
+              const uint64_t x =
+                  fma2(pack2(make_float2(s[c + 2 * e], s[c + 2 * e + 1])), scale2, neg_m2);
               float2 pe;
               if (e % 4 < kPolyOfFour) {
                 pe = exp2_poly(x);
@@ -790,10 +801,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
             tmem_st16(s_addr + uint32_t(c / 2), p);
           }
-          {
-            const float2 t = unpack2(add2(sum_a, sum_b));
-            l += t.x + t.y;
-          }
+          const float2 t = unpack2(add2(sum_a, sum_b));
+          l += t.x + t.y;
           tmem_wait_st();
           tc_fence_before();
         }
@@ -802,55 +811,66 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
       if (!ok) break;
       // ---- the unit's rows (or this segment's part of them) ----
-      if (!warp_wait(&o_full[w], no & 1, a.status, &abort_s)) break;
+      // (the products that complete here waited for the other warp's weights,
+      // so it has read this row's maximum)
+      const bool fail = !warp_wait(&o_full[w], no & 1, a.status, &abort_s);
+      half_row[w][half][row] = l;
+      if (named_bar_or(pair_bar, 64, fail)) break;
       ++no;
       if (busy) {
         tc_fence_after();
-        const bool mine = tok < g.ntok;
-        if (g.type == kWhole) {
-          const int64_t r = (g.tok0 + tok) * a.hq + g.h * group + row % group;
+        l += half_row[w][half ^ 1][row];
+        // (read again: nothing but the loop's own state stays in registers)
+        const int type = seg_q[qs].type;
+        const int64_t tok0 = seg_q[qs].tok0;
+        const bool mine = tok < seg_q[qs].ntok;
+        const int d0 = half * (D / 2);
+        if (type == kWhole) {
+          const int64_t r = (tok0 + tok) * a.hq + seg_q[qs].h * group + row % group;
           const bool some = m != -INFINITY;           // the row has a key
           const float inv = some ? 1.f / l : 0.f;
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < D / 2; c += 32) {
             float o[32];
             tmem_ld32(o_addr + c, o);
             if (mine) {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + r * D + c);
+              uint4* dst = reinterpret_cast<uint4*>(a.out + r * D + d0 + c);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t v[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                   v[x] = some ? bf16x2_bits(o[8 * e + 2 * x] * inv, o[8 * e + 2 * x + 1] * inv)
-                                 : 0u;
+                              : 0u;
                 dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
               }
             }
           }
-          if (mine && a.lse != nullptr)
+          if (mine && half == 0 && a.lse != nullptr)
             a.lse[r] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
         } else {
-          float* part = slot_rows(a, D, 2 * int64_t(blockIdx.x) + (g.type == kBegin ? 1 : 0));
+          float* part = slot_rows(a, D, 2 * int64_t(blockIdx.x) + (type == kBegin ? 1 : 0));
           const int r = w * kTileRows + row;
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < D / 2; c += 32) {
             float o[32];
             tmem_ld32(o_addr + c, o);
             if (mine) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                reinterpret_cast<float4*>(part)[(c / 4 + e) * kUnitRows + r] =
+                reinterpret_cast<float4*>(part)[((d0 + c) / 4 + e) * kUnitRows + r] =
                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
           }
-          if (mine) {
+          if (mine && half == 0) {
             part[kUnitRows * D + r] = m;
             part[kUnitRows * (D + 1) + r] = l;
           }
         }
         tc_fence_before();
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[qs]);
     }
   }
   tc_fence_before();
