@@ -42,13 +42,13 @@
 namespace cobs {
 namespace {
 
-constexpr int kThreads = 640;            // four softmax warpgroups, one for the rest
-constexpr int kSoftWarps = 16;
-constexpr int kProducerWarp = 16, kMmaWarp = 17;
-// Registers: 640 x 96 at launch, of which the softmax threads (half a row of
-// scores each) take 104 and the others keep 64.
-constexpr int kSoftRegs = 104, kOtherRegs = 64;
-static_assert(512 * kSoftRegs + 128 * kOtherRegs <= 640 * 96, "register split");
+constexpr int kThreads = 384;            // two softmax warpgroups, one for the rest
+constexpr int kSoftWarps = 8;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+// Registers: 384 x 168 at launch, of which the softmax threads (a row of 128
+// scores each) take 208 and the others keep 80.
+constexpr int kSoftRegs = 208, kOtherRegs = 80;
+static_assert(32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 constexpr int kTileRows = 128;
 constexpr int kKeyShift = 7;
 constexpr int kKeys = 1 << kKeyShift;    // keys per iteration
@@ -60,7 +60,6 @@ constexpr int kMinShare = 4;             // iterations of a share, at least
 constexpr int kSegQ = 2;                 // segments handed from the producer to the others
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kTmemCols = 512;      // S0, S1 (P over them), O0, O1
-constexpr int kPolyOfFour = 1;           // of four pairs of weights, those by exp2_poly
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D>
@@ -68,7 +67,7 @@ struct Tile {
   static constexpr int kSlabs = D / 64;
   static constexpr int kSlabBytes = 128 * 128;          // 128 rows x 64 columns bf16
   static constexpr int kBytes = kSlabs * kSlabBytes;
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kOffQ = kStages * kBytes;
   static constexpr int kDynSmem = kOffQ + 2 * kBytes + 1024;
 };
@@ -315,28 +314,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 2^x of a pair on the fused multiply-add pipe, x <= 9, below -126 taken as
-// -126: x = n + r with n = round(x) from the low bits of x + 1.5 2^23 and
-// |r| <= 1/2, 2^r by the cubic whose relative error is smallest on that
-// interval (equal-ripple fit, 7.5e-5 = 2^-13.7; a weight is rounded to bf16,
-// 2^-8, afterwards), n added to the exponent bits.
-__device__ __forceinline__ float2 exp2_poly(uint64_t x2) {
-  float2 x = unpack2(x2);
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
-  x2 = pack2(x);
-  auto both = [](float v) { return pack2(make_float2(v, v)); };
-  const uint64_t t = add2(x2, both(12582912.f));
-  const uint64_t r = fma2(add2(t, both(-12582912.f)), both(-1.f), x2);
-  uint64_t y = fma2(both(0.0551716685f), r, both(0.242611125f));
-  y = fma2(y, r, both(0.693260968f));
-  y = fma2(y, r, both(0.999928057f));
-  const float2 tv = unpack2(t), yv = unpack2(y);
-  return make_float2(
-      __uint_as_float((__float_as_uint(tv.x) << 23) + __float_as_uint(yv.x)),
-      __uint_as_float((__float_as_uint(tv.y) << 23) + __float_as_uint(yv.y)));
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -378,13 +355,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   __shared__ __align__(8) uint64_t full[kStages];
   __shared__ __align__(8) uint64_t empty[kStages];
   __shared__ __align__(8) uint64_t q_full, q_empty, v_tail, drain;
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_full[2];   // p: halves of the keys
+  __shared__ __align__(8) uint64_t ml_full, ml_free;   // one tile: the second stream's sums
   __shared__ __align__(8) uint64_t seg_full[kSegQ], seg_empty[kSegQ];
   __shared__ Segment seg_q[kSegQ];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_s;
   __shared__ Share share;
-  __shared__ float half_row[2][2][kTileRows];   // a tile's row over half its keys: max, sum
+  __shared__ float other_ml[2][kTileRows];   // one tile: the second stream's maxima, sums
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane
@@ -403,9 +381,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     mbar_init(&q_empty, 1);
     mbar_init(&v_tail, 1);
     mbar_init(&drain, 1);
+    mbar_init(&ml_full, 4);
+    mbar_init(&ml_free, 4);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 8);
+      mbar_init(&p_full[w][0], 4);
+      mbar_init(&p_full[w][1], 4);
       mbar_init(&o_full[w], 1);
     }
     for (int s = 0; s < kSegQ; ++s) {
@@ -606,9 +587,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     };
     // (a descriptor's address field counts 16 bytes; shared memory ends
     // below 2^18, so adding to it never carries out of its 14 bits)
-    auto qk = [&](auto wc, uint32_t st) {
+    // S of stream wc = Q of tile qt times the keys in ring slot st
+    auto qk = [&](auto wc, int qt, uint32_t st) {
       constexpr int w = decltype(wc)::value;
-      const uint64_t qd = umma_desc_sw128(q0 + w * T::kBytes);
+      const uint64_t qd = umma_desc_sw128(q0 + qt * T::kBytes);
       const uint64_t kd = umma_desc_sw128(ring0 + st * T::kBytes);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
@@ -618,14 +600,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       umma_commit_if(elected, &s_full[w]);
       issued = true;
     };
-    auto pv = [&](auto wc, uint32_t st, uint32_t accumulate) {
+    auto pv = [&](auto wc, uint32_t st, uint32_t accumulate, uint32_t parity) {
       constexpr int w = decltype(wc)::value;
       const uint64_t vd = umma_desc_sw128_mn(ring0 + st * T::kBytes, T::kSlabBytes);
 #pragma unroll
-      for (int ks = 0; ks < kKeys / 16; ++ks)
-        umma_bf16_ta_if(elected, tmem + 256u + uint32_t(D) * w,
-                        tmem + 128u * w + (ks >> 2) * 64u + (ks & 3) * 8u,
-                        vd + ks * (2048 >> 4), idesc_pv, ks > 0 ? 1u : accumulate);
+      for (int half = 0; half < 2; ++half) {
+        if (!wait(&p_full[w][half], parity)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+          umma_bf16_ta_if(elected, tmem + 256u + uint32_t(D) * w, tmem + 128u * w + 8u * ks,
+                          vd + ks * (2048 >> 4), idesc_pv, ks > 0 ? 1u : accumulate);
+      }
+      return true;
     };
     const Index<0> tile0;
     const Index<1> tile1;
@@ -639,46 +626,75 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       __syncwarp();
       if (type == kNone) break;
       const bool two = ntok > tt;
-      uint32_t kst = item % kStages;
-      if (!wait(&q_full, nseg & 1) || !wait(&full[kst], (item / kStages) & 1)) break;
+      const uint32_t item0 = item;       // K_i is ring item item0 + 2 i, V_i the next
+      auto slot_of = [&](uint32_t x) { return x % kStages; };
+      auto wait_item = [&](uint32_t x) {
+        const bool r = wait(&full[x % kStages], (x / kStages) & 1);
+        if (r) tc_fence_after();
+        return r;
+      };
+      if (!wait(&q_full, nseg & 1) || !wait_item(item0)) break;
       ++nseg;
-      tc_fence_after();
-      qk(tile0, kst);
-      if (two) qk(tile1, kst);
-      umma_commit_if(elected, &empty[kst]);
+      qk(tile0, 0, slot_of(item0));
+      if (two) qk(tile1, 1, slot_of(item0));
+      umma_commit_if(elected, &empty[slot_of(item0)]);
       if (n_it == 1) umma_commit_if(elected, &q_empty);
-      for (int i = 0; i < n_it; ++i) {
-        const uint32_t vi = item + 1, vst = vi % kStages;
-        const bool more = i + 1 < n_it;
-        item += 2;
-        kst = item % kStages;
-        ok = wait(&full[vst], (vi / kStages) & 1) && wait(&p_full[0], np0 & 1);
-        if (!ok) break;
-        ++np0;
-        tc_fence_after();
-        pv(tile0, vst, i > 0 ? 1u : 0u);
-        if (!two) umma_commit_if(elected, &empty[vst]);
-        if (more) {
-          ok = wait(&full[kst], (item / kStages) & 1);
+      item += 2u * uint32_t(n_it);
+      if (two) {
+        // both tiles, every iteration
+        for (int i = 0; i < n_it; ++i) {
+          const uint32_t vi = item0 + 2u * i + 1u, ki = vi + 1u;
+          const bool more = i + 1 < n_it;
+          ok = wait_item(vi) && pv(tile0, slot_of(vi), i > 0 ? 1u : 0u, np0 & 1);
           if (!ok) break;
-          tc_fence_after();
-          qk(tile0, kst);
-        } else {
-          umma_commit_if(elected, &o_full[0]);
-        }
-        if (two) {
-          ok = wait(&p_full[1], np1 & 1);
+          ++np0;
+          if (more) {
+            ok = wait_item(ki);
+            if (!ok) break;
+            qk(tile0, 0, slot_of(ki));
+          } else {
+            umma_commit_if(elected, &o_full[0]);
+          }
+          ok = pv(tile1, slot_of(vi), i > 0 ? 1u : 0u, np1 & 1);
           if (!ok) break;
           ++np1;
-          tc_fence_after();
-          pv(tile1, vst, i > 0 ? 1u : 0u);
-          umma_commit_if(elected, &empty[vst]);
-          if (more) qk(tile1, kst);
-          else umma_commit_if(elected, &o_full[1]);
+          umma_commit_if(elected, &empty[slot_of(vi)]);
+          if (more) {
+            qk(tile1, 1, slot_of(ki));
+            umma_commit_if(elected, &empty[slot_of(ki)]);
+            if (i + 2 == n_it) umma_commit_if(elected, &q_empty);
+          } else {
+            umma_commit_if(elected, &o_full[1]);
+          }
         }
-        if (more) {
-          umma_commit_if(elected, &empty[kst]);
-          if (i + 2 == n_it) umma_commit_if(elected, &q_empty);
+      } else {
+        // one tile: stream 0 takes its even iterations, stream 1 the odd ones
+        if (n_it > 1) {
+          ok = wait_item(item0 + 2u);
+          if (!ok) break;
+          qk(tile1, 0, slot_of(item0 + 2u));
+          umma_commit_if(elected, &empty[slot_of(item0 + 2u)]);
+          if (n_it == 2) umma_commit_if(elected, &q_empty);
+        }
+        auto step = [&](auto wc, int i, uint32_t& np) {
+          constexpr int w = decltype(wc)::value;
+          const uint32_t vi = item0 + 2u * i + 1u, ki = vi + 3u;   // V_i, K_{i + 2}
+          if (!wait_item(vi) || !pv(wc, slot_of(vi), i > 1 ? 1u : 0u, np & 1)) return false;
+          ++np;
+          umma_commit_if(elected, &empty[slot_of(vi)]);
+          if (i + 2 < n_it) {
+            if (!wait_item(ki)) return false;
+            qk(wc, 0, slot_of(ki));
+            umma_commit_if(elected, &empty[slot_of(ki)]);
+            if (i + 3 == n_it) umma_commit_if(elected, &q_empty);
+          } else {
+            umma_commit_if(elected, &o_full[w]);
+          }
+          return true;
+        };
+        for (int i = 0; i < n_it && ok; i += 2) {
+          ok = step(tile0, i, np0);
+          if (ok && i + 1 < n_it) ok = step(tile1, i + 1, np1);
         }
       }
     }
@@ -691,186 +707,212 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ======================= softmax and output ===========================
-    const int w = warp >> 3, half = (warp >> 2) & 1;
+    const int w = warp >> 2;
     const int row = (warp & 3) * 32 + lane;         // of the tile
-    const int pair_bar = 1 + w * 4 + (warp & 3);    // the two warps of these rows
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    // this thread's 64 scores; its weights overwrite the first 32 columns
-    const uint32_t s_addr = tmem + lane_base + 128u * w + 64u * half;
-    const uint32_t o_addr = tmem + lane_base + 256u + uint32_t(D) * w + uint32_t(D / 2) * half;
-    const int tok = w * tt + row / group;           // token of the unit
-    const int tok_w = w * tt + (warp & 3) * 32 / group;   // the warp's first
-    uint32_t nseg = 0, ns = 0, no = 0;
+    const uint32_t s_addr = tmem + lane_base + 128u * w;   // weights over the first 64 columns
+    const uint32_t o_addr = tmem + lane_base + 256u + uint32_t(D) * w;
+    const uint64_t scale2 = pack2(make_float2(a.scale_log2, a.scale_log2));
+    uint32_t nseg = 0, ns = 0, no = 0, joins = 0;
     bool ok = true;
     for (; ok; ++nseg) {
       const int qs = nseg % kSegQ;
-      const bool got = warp_wait(&seg_full[qs], (nseg / kSegQ) & 1, a.status, &abort_s);
-      // the two warps of a row go on together or give up together
-      if (named_bar_or(pair_bar, 64, !got)) break;
-      const bool here = w * tt < seg_q[qs].ntok;  // the tile has rows
-      const bool busy = tok_w < seg_q[qs].ntok;   // a row of the warp is a token's
+      if (!warp_wait(&seg_full[qs], (nseg / kSegQ) & 1, a.status, &abort_s)) break;
       if (seg_q[qs].type == kNone) break;
-      if (!here) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[qs]);
-        continue;
-      }
+      // two tiles: each warpgroup has one; one tile: both have its rows, and
+      // every second iteration
+      const bool two = seg_q[qs].ntok > tt;
+      const int tok = (two ? w * tt : 0) + row / group;   // token of the unit
+      const int tok_w = (two ? w * tt : 0) + (warp & 3) * 32 / group;   // the warp's first
+      const bool busy = tok_w < seg_q[qs].ntok;   // a row of the warp is a token's
       const int it0 = seg_q[qs].it0, it1 = seg_q[qs].it1;
       const int pos = int(seg_q[qs].pos0) + tok;
       const int blocks = int((seg_q[qs].len + kBlock - 1) / kBlock);
       const int32_t* table =
-          kPaged ? a.c.table + int64_t(seg_q[qs].b) * a.c.table_stride + half : nullptr;
+          kPaged ? a.c.table + int64_t(seg_q[qs].b) * a.c.table_stride : nullptr;
       float m = -INFINITY, l = 0.f;
-      for (int i = it0; i < it1; ++i, ++ns) {
-        // (paged) this half's block has no page: its keys are not there
-        bool gone = false;
+      const int first = two ? it0 : it0 + w, step = two ? 1 : 2;
+      for (int i = first; i < it1; i += step, ++ns) {
+        // (paged) blocks without a page: their keys are not there
+        uint32_t gone = 0;
         if constexpr (kPaged) {
-          if (busy && 2 * i + half < blocks) {
-            const int32_t p = __ldg(table + 2 * i);
-            gone = p < 0 || p >= a.c.n_pages;
+          bool bad = false;
+          if (busy && lane < 2 && 2 * i + lane < blocks) {
+            const int32_t p = __ldg(table + 2 * i + lane);
+            bad = p < 0 || p >= a.c.n_pages;
           }
+          gone = __ballot_sync(0xffffffffu, bad);
         }
-        const bool fail = !warp_wait(&s_full[w], ns & 1, a.status, &abort_s);
-        float s[64];
-        float mx = -INFINITY;
-        if (busy && !fail) {
-          tc_fence_after();
-          tmem_ld32_nowait(s_addr, s);
-          tmem_ld32_nowait(s_addr + 32u, s + 32);
-          tmem_wait_ld();
-          // the last key this row sees, among these 64
-          const int lim = gone ? -1 : pos - i * kKeys - 64 * half;
-          if (__any_sync(0xffffffffu, lim < 63)) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = c > lim ? -INFINITY : s[c];
-          }
-          float mx1 = fmaxf(s[2], s[3]);
-          mx = fmaxf(s[0], s[1]);
-#pragma unroll
-          for (int c = 4; c < 64; c += 4) {
-            mx = max3(mx, s[c], s[c + 1]);
-            mx1 = max3(mx1, s[c + 2], s[c + 3]);
-          }
-          mx = fmaxf(mx, mx1);
-          half_row[w][half][row] = mx;
-        }
-        if (named_bar_or(pair_bar, 64, fail)) {
+        if (!warp_wait(&s_full[w], ns & 1, a.status, &abort_s)) {
           ok = false;
           break;
         }
         if (busy) {
-          mx = fmaxf(mx, half_row[w][half ^ 1][row]) * a.scale_log2;
-          const bool raise = mx > m + kRescaleLog2;   // also the first key of a row
-          if (__any_sync(0xffffffffu, raise)) {
-            const float mn = raise ? mx : m;
-            const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
-            m = mn;
-            l *= alpha;
-            if (i > it0) {
+          tc_fence_after();
+          float s[kKeys];
 #pragma unroll
-              for (int c = 0; c < D / 2; c += 16) {   // narrow: 64 scores are live
+          for (int c = 0; c < kKeys; c += 32) tmem_ld32_nowait(s_addr + c, s + c);
+          tmem_wait_ld();
+          const int lim = pos - i * kKeys;   // the last key that this row sees
+          if (__any_sync(0xffffffffu, lim < kKeys - 1) || (kPaged && gone != 0)) {
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              if (c > lim || (kPaged && ((gone >> (c >> 6)) & 1u))) s[c] = -INFINITY;
+          }
+          auto row_max = [&]() {
+            float m0 = fmaxf(s[0], s[1]), m1 = fmaxf(s[2], s[3]);
+#pragma unroll
+            for (int c = 4; c < kKeys; c += 4) {
+              m0 = max3(m0, s[c], s[c + 1]);
+              m1 = max3(m1, s[c + 2], s[c + 3]);
+            }
+            return fmaxf(m0, m1) * a.scale_log2;
+          };
+          // weights 2^(s - m) of 64 keys into tensor memory; returns their sum
+          auto weights = [&](int c0) {
+            const float neg_m = m == -INFINITY ? 0.f : -m;
+            const uint64_t neg_m2 = pack2(make_float2(neg_m, neg_m));
+            uint64_t sum_a = 0, sum_b = 0;
+#pragma unroll
+            for (int c = c0; c < c0 + 64; c += 32) {
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float2 pe = unpack2(
+                    fma2(pack2(make_float2(s[c + 2 * e], s[c + 2 * e + 1])), scale2, neg_m2));
+                pe = make_float2(hw_exp2(pe.x), hw_exp2(pe.y));
+                if (e & 1) sum_b = add2(sum_b, pack2(pe));
+                else sum_a = add2(sum_a, pack2(pe));
+                p[e] = bf16x2_bits(pe.x, pe.y);
+              }
+              tmem_st16(s_addr + uint32_t(c / 2), p);
+            }
+            const float2 t = unpack2(add2(sum_a, sum_b));
+            return t.x + t.y;
+          };
+          auto release = [&](int half) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[w][half]);
+          };
+          float sum;
+          if (i == first) {
+            m = row_max();
+            sum = weights(0);
+          } else {
+            // The first half with the maximum as it was: it moves so rarely
+            // that the weights are formed while the new one is still being
+            // found, and again in the case that it did move.
+            sum = weights(0);
+            const float mx = row_max();
+            const bool raise = mx > m + kRescaleLog2;
+            if (__any_sync(0xffffffffu, raise)) {
+              const float mn = raise ? mx : m;
+              const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
+              m = mn;
+              l *= alpha;
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {   // narrow: 128 scores are live
                 float o[16];
                 tmem_ld16(o_addr + c, o);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] *= alpha;
                 tmem_st16(o_addr + c, reinterpret_cast<const uint32_t*>(o));
               }
+              sum = weights(0);
             }
           }
-          const float neg_m = m == -INFINITY ? 0.f : -m;
-          const uint64_t scale2 = pack2(make_float2(a.scale_log2, a.scale_log2));
-          const uint64_t neg_m2 = pack2(make_float2(neg_m, neg_m));
-          uint64_t sum_a = 0, sum_b = 0;
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint64_t x =
-                  fma2(pack2(make_float2(s[c + 2 * e], s[c + 2 * e + 1])), scale2, neg_m2);
-              float2 pe;
-              if (e % 4 < kPolyOfFour) {
-                pe = exp2_poly(x);
-              } else {
-                const float2 xv = unpack2(x);
-                pe = make_float2(hw_exp2(xv.x), hw_exp2(xv.y));
-              }
-              if (e & 1) sum_b = add2(sum_b, pack2(pe));
-              else sum_a = add2(sum_a, pack2(pe));
-              p[e] = bf16x2_bits(pe.x, pe.y);
-            }
-            tmem_st16(s_addr + uint32_t(c / 2), p);
-          }
-          const float2 t = unpack2(add2(sum_a, sum_b));
-          l += t.x + t.y;
-          tmem_wait_st();
-          tc_fence_before();
+          release(0);
+          l += sum + weights(64);
+          release(1);
+        } else if (lane == 0) {
+          mbar_arrive(&p_full[w][0]);
+          mbar_arrive(&p_full[w][1]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
       }
       if (!ok) break;
       // ---- the unit's rows (or this segment's part of them) ----
-      // (the products that complete here waited for the other warp's weights,
-      // so it has read this row's maximum)
-      const bool fail = !warp_wait(&o_full[w], no & 1, a.status, &abort_s);
-      half_row[w][half][row] = l;
-      if (named_bar_or(pair_bar, 64, fail)) break;
-      ++no;
-      if (busy) {
+      if (first < it1) {
+        if (!warp_wait(&o_full[w], no & 1, a.status, &abort_s)) break;
+        ++no;
+      }
+      float m1 = -INFINITY, l1 = 0.f;    // one tile: the other stream's part of the row
+      if (!two && w == 1) {
+        // handed to the first warpgroup, which also reads this stream's O
+        other_ml[0][row] = m;
+        other_ml[1][row] = l;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ml_full);
+        if (!warp_wait(&ml_free, joins & 1, a.status, &abort_s)) break;
+      } else if (!two) {
+        if (!warp_wait(&ml_full, joins & 1, a.status, &abort_s)) break;
+        m1 = other_ml[0][row];
+        l1 = other_ml[1][row];
+      }
+      if (busy && (two || w == 0)) {
         tc_fence_after();
-        l += half_row[w][half ^ 1][row];
         // (read again: nothing but the loop's own state stays in registers)
         const int type = seg_q[qs].type;
         const int64_t tok0 = seg_q[qs].tok0;
         const bool mine = tok < seg_q[qs].ntok;
-        const int d0 = half * (D / 2);
-        if (type == kWhole) {
-          const int64_t r = (tok0 + tok) * a.hq + seg_q[qs].h * group + row % group;
-          const bool some = m != -INFINITY;           // the row has a key
-          const float inv = some ? 1.f / l : 0.f;
+        const float mm = fmaxf(m, m1);
+        const bool some = mm != -INFINITY;           // the row has a key
+        const float w0 = m != -INFINITY ? hw_exp2(m - mm) : 0.f;
+        const float w1 = m1 != -INFINITY ? hw_exp2(m1 - mm) : 0.f;
+        const float ll = l * w0 + l1 * w1;
+        const float inv = type == kWhole ? (some ? 1.f / ll : 0.f) : 1.f;
+        const float f0 = w0 * inv, f1 = w1 * inv;
+        const int64_t r = (tok0 + tok) * a.hq + seg_q[qs].h * group + row % group;
+        float* part = slot_rows(a, D, 2 * int64_t(blockIdx.x) + (type == kBegin ? 1 : 0));
+        const int pr = (two ? w * kTileRows : 0) + row;
+        // (not from f1 alone: rows of nobody may hold NaN, and the second tile
+        // has no columns after its own)
+        const bool both = !two && __any_sync(0xffffffffu, m1 != -INFINITY);
 #pragma unroll
-          for (int c = 0; c < D / 2; c += 32) {
-            float o[32];
-            tmem_ld32(o_addr + c, o);
-            if (mine) {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + r * D + d0 + c);
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          __syncwarp();   // rows of nobody skip the stores: together again for the load
+          tmem_ld32(o_addr + c, o);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t v[4];
+          for (int e = 0; e < 32; ++e) o[e] = f0 != 0.f ? o[e] * f0 : 0.f;
+          if (both) {
+            float o1[32];
+            tmem_ld32(o_addr + uint32_t(D) + c, o1);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  v[x] = some ? bf16x2_bits(o[8 * e + 2 * x] * inv, o[8 * e + 2 * x + 1] * inv)
-                              : 0u;
-                dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-            }
+            for (int e = 0; e < 32; ++e) o[e] = f1 != 0.f ? fmaf(o1[e], f1, o[e]) : o[e];
           }
-          if (mine && half == 0 && a.lse != nullptr)
-            a.lse[r] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
-        } else {
-          float* part = slot_rows(a, D, 2 * int64_t(blockIdx.x) + (type == kBegin ? 1 : 0));
-          const int r = w * kTileRows + row;
+          if (mine && type == kWhole) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + r * D + c);
 #pragma unroll
-          for (int c = 0; c < D / 2; c += 32) {
-            float o[32];
-            tmem_ld32(o_addr + c, o);
-            if (mine) {
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(bf16x2_bits(o[8 * e], o[8 * e + 1]),
+                                  bf16x2_bits(o[8 * e + 2], o[8 * e + 3]),
+                                  bf16x2_bits(o[8 * e + 4], o[8 * e + 5]),
+                                  bf16x2_bits(o[8 * e + 6], o[8 * e + 7]));
+          } else if (mine) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<float4*>(part)[((d0 + c) / 4 + e) * kUnitRows + r] =
-                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(part)[(c / 4 + e) * kUnitRows + pr] =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
-          if (mine && half == 0) {
-            part[kUnitRows * D + r] = m;
-            part[kUnitRows * (D + 1) + r] = l;
-          }
+        }
+        if (mine && type == kWhole) {
+          if (a.lse != nullptr) a.lse[r] = some ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+        } else if (mine) {
+          part[kUnitRows * D + pr] = mm;
+          part[kUnitRows * (D + 1) + pr] = ll;
         }
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_empty[qs]);
+      if (lane == 0) {
+        if (!two && w == 0) mbar_arrive(&ml_free);
+        mbar_arrive(&seg_empty[qs]);
+      }
+      joins += two ? 0u : 1u;
     }
   }
   tc_fence_before();
