@@ -237,6 +237,14 @@ cudaError_t make_bf16_tensor_map_3d_sw128_box(CUtensorMap* map, const void* base
                                               uint64_t stride1_bytes, uint64_t stride2_bytes,
                                               int box1, int box2);
 
+// Host: 3-d tensor map over `depth` matrices of [rows][cols] bytes that sit
+// `depth_stride_bytes` apart, box of 128 columns x box_rows rows x 1, 128-byte
+// swizzle.  Columns at or past `cols` (a multiple of 16) and rows at or past
+// `rows` read as zero.
+cudaError_t make_byte_tensor_map_3d_sw128(CUtensorMap* map, const void* base, int cols,
+                                          uint64_t rows, uint64_t depth,
+                                          uint64_t depth_stride_bytes, int box_rows);
+
 // Host: 3-d tensor map (component, row, record) over packed E2M1 codes (two
 // per byte, `cols` components a row, rows `stride1_bytes` apart, records
 // `stride2_bytes` apart; base 32-byte aligned, strides multiples of 32, cols

@@ -89,6 +89,22 @@ cudaError_t make_bf16_tensor_map_3d_sw128_box(CUtensorMap* map, const void* base
   return cudaSuccess;
 }
 
+cudaError_t make_byte_tensor_map_3d_sw128(CUtensorMap* map, const void* base, int cols,
+                                          uint64_t rows, uint64_t depth,
+                                          uint64_t depth_stride_bytes, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(depth)};
+  const cuuint64_t strides[2] = {cuuint64_t(cols), cuuint64_t(depth_stride_bytes)};
+  const cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
 cudaError_t make_e2m1_unpacked_tensor_map_3d_sw128(CUtensorMap* map, const void* base, int cols,
                                                    uint64_t dim1, uint64_t dim2,
                                                    uint64_t stride1_bytes,

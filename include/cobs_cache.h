@@ -195,9 +195,10 @@ COBS_API cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_
  *   logit_j = softmax_scale * k_scale_j * (q . k_code_j),
  *   out = sum_j e^(logit_j - m) v_scale_j v_code_j / sum_j e^(logit_j - m),
  * with q split into three E4M3 parts that hold every component exactly down
- * to 2^-18 of the row's largest (components below it are rounded by at most
- * 2^-26 of the largest), and the weights rounded by at most 2^-16 of
- * themselves.  Codes of tokens inside a sequence must not be NaN.
+ * to 2^-16 of the row's largest (components below it are rounded by at most
+ * 2^-24 of the largest), and each weight e^(logit_j - m) v_scale_j rounded by
+ * at most 2^-16 of itself or 2^-22 of the pair's largest, whichever is more.
+ * Codes of tokens inside a sequence must not be NaN.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 COBS_API cobs_status cobs_sparse_decode_cache(const cobs_dims* dims, const cobs_kv_cache* cache,
                                               const void* q, const int32_t* idx,

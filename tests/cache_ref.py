@@ -88,17 +88,23 @@ class Cache:
                 pool[self.table[b, j], :, :rows.shape[1]] = rows
         return pool
 
+    def part(self, name, b, h, n):
+        """First n logical rows of an array of the cache."""
+        x = self.parts[name]
+        if self.table is None:
+            return x[b, h, :n]
+        nb = -(-n // B)
+        return x[self.table[b, :nb].long(), h].flatten(0, 1)[:n]
+
+    def scales(self, name, b, h, n):
+        return self.part(name + "s", b, h, n).double()
+
     def rows(self, name, b, h, n):
         """First n logical rows of (sequence b, kv-head h), in 64 bits."""
-        def get(part):
-            x = self.parts[part]
-            if self.table is None:
-                return x[b, h, :n]
-            nb = -(-n // B)
-            return x[self.table[b, :nb].long(), h].flatten(0, 1)[:n]
-        x = get(name)
+        x = self.part(name, b, h, n)
         if self.e4m3:
-            return x.contiguous().view(torch.float8_e4m3fn).double() * get(name + "s").double()[:, None]
+            codes = x.contiguous().view(torch.float8_e4m3fn).double()
+            return codes * self.scales(name, b, h, n)[:, None]
         return x.double()
 
 
