@@ -384,16 +384,39 @@ def cobs_set_wait_limit_ns(limit_ns: int) -> int:
     return _check("cobs_set_wait_limit_ns", lib.cobs_set_wait_limit_ns(int(limit_ns)), True)
 
 
-def _rows_ptr(x, stride, name):
+def _addr(x):
+    """Like _ptr, as a plain integer or None."""
+    if x is None or type(x) is int:
+        return x
+    try:
+        if x.is_cuda and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(x).value
+
+
+def _rows_addr(x, stride, name):
     """Address of packed rows that start ``stride`` elements apart: a CUDA
     tensor whose rows are contiguous and lie that far apart (a part of a fused
     projection), an address or None."""
-    if not hasattr(x, "data_ptr"):
-        return _ptr(x)
+    if x is None or type(x) is int:
+        return x
+    try:
+        st, shape = x.stride(), x.shape
+    except AttributeError:
+        return _ptr(x).value
+    if len(st) == 3 and st[2] == 1 and st[1] == shape[2] and st[0] == stride and x.is_cuda:
+        return x.data_ptr()
     if not x.is_cuda:
         raise TypeError("tensor arguments must be CUDA tensors (got a host tensor)")
-    if x.shape[0] > 1 and x.stride(0) != stride or x.shape[0] > 0 and not x[0].is_contiguous():
-        raise TypeError(f"{name}: rows must be contiguous and {name}_stride elements apart")
+    row = 1
+    for n, s in zip(shape[:0:-1], st[:0:-1]):
+        if s != row and n > 1:
+            raise TypeError(f"{name}: rows must be contiguous")
+        row *= n
+    if st[0] != stride and shape[0] > 1:
+        raise TypeError(f"{name}: rows must be {name}_stride elements apart")
     return x.data_ptr()
 
 
@@ -424,10 +447,10 @@ def cobs_append_tokens(dims, cache, rope, q, q_stride, k, k_stride, v, v_stride,
     q, k and v may be parts of one fused projection (rows q_stride, ... apart);
     rope and q (with q_out) may be None."""
     st = lib.cobs_append_tokens(ctypes.byref(_dims(dims)), _ref(cache), _ref(rope),
-                                _rows_ptr(q, q_stride, "q"), q_stride,
-                                _rows_ptr(k, k_stride, "k"), k_stride,
-                                _rows_ptr(v, v_stride, "v"), v_stride, _ptr(cu_tokens),
-                                n_tokens, _ptr(start), _ptr(q_out), _ptr(ws), ws_bytes,
+                                _rows_addr(q, q_stride, "q"), q_stride,
+                                _rows_addr(k, k_stride, "k"), k_stride,
+                                _rows_addr(v, v_stride, "v"), v_stride, _addr(cu_tokens),
+                                n_tokens, _addr(start), _addr(q_out), _addr(ws), ws_bytes,
                                 _stream(stream))
     return _check("cobs_append_tokens", st, check)
 
@@ -436,8 +459,8 @@ def cobs_read_cache(dims, cache, seq_lens, block_begin, block_end, k_out, v_out,
                     stream=None, check=True) -> int:
     """Blocks of a cache of either format as bf16 pages (seq_lens, k_out or v_out
     may be None)."""
-    st = lib.cobs_read_cache(ctypes.byref(_dims(dims)), _ref(cache), _ptr(seq_lens),
-                             block_begin, block_end, _ptr(k_out), _ptr(v_out), _ptr(ws),
+    st = lib.cobs_read_cache(ctypes.byref(_dims(dims)), _ref(cache), _addr(seq_lens),
+                             block_begin, block_end, _addr(k_out), _addr(v_out), _addr(ws),
                              ws_bytes, _stream(stream))
     return _check("cobs_read_cache", st, check)
 
@@ -454,9 +477,9 @@ def cobs_prompt_attention(dims, cache, q, cu_tokens, n_tokens, seq_lens, max_seq
                           check=True) -> int:
     """Causal attention of the packed new tokens over the bf16 cache that holds
     them (cu_tokens None: one token per sequence; lse may be None)."""
-    st = lib.cobs_prompt_attention(ctypes.byref(_dims(dims)), _ref(cache), _ptr(q),
-                                   _ptr(cu_tokens), n_tokens, _ptr(seq_lens), max_seq_len,
-                                   softmax_scale, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+    st = lib.cobs_prompt_attention(ctypes.byref(_dims(dims)), _ref(cache), _addr(q),
+                                   _addr(cu_tokens), n_tokens, _addr(seq_lens), max_seq_len,
+                                   softmax_scale, _addr(out), _addr(lse), _addr(ws), ws_bytes,
                                    _stream(stream))
     return _check("cobs_prompt_attention", st, check)
 
@@ -466,8 +489,8 @@ def cobs_sparse_decode_cache(dims, cache, q, idx, n_sel, idx_stride, seq_lens, m
                              check=True) -> int:
     """cobs_sparse_decode over a cache of either format, contiguous or paged
     (seq_lens None: every sequence is max_seq_len tokens long)."""
-    st = lib.cobs_sparse_decode_cache(ctypes.byref(_dims(dims)), _ref(cache), _ptr(q),
-                                      _ptr(idx), _ptr(n_sel), idx_stride, _ptr(seq_lens),
-                                      max_seq_len, softmax_scale, _ptr(out), _ptr(lse),
-                                      _ptr(ws), ws_bytes, _stream(stream))
+    st = lib.cobs_sparse_decode_cache(ctypes.byref(_dims(dims)), _ref(cache), _addr(q),
+                                      _addr(idx), _addr(n_sel), idx_stride, _addr(seq_lens),
+                                      max_seq_len, softmax_scale, _addr(out), _addr(lse),
+                                      _addr(ws), ws_bytes, _stream(stream))
     return _check("cobs_sparse_decode_cache", st, check)

@@ -11,14 +11,21 @@
 //
 // Bound by memory: every row is read once and written once.  A warp takes
 // some head rows of one token, so the sines and cosines (they depend on the
-// token alone) are computed once for all of them; d / 8 lanes share a row,
-// each with four pairs, in two 8-byte pieces.
+// token alone), the sequence and the page are found once for all of them;
+// d / 8 lanes share a row, each with four pairs, in two 8-byte pieces, and
+// the loads of kBatch rows are issued together.
 #include "cache_device.cuh"
 
 namespace cobs {
 namespace {
 
 constexpr int kAppendWarps = 4;
+constexpr int kBatch = 4;                // rows (of a sub-warp) loaded together
+
+template <int K>
+struct Kind {
+  static constexpr int value = K;
+};
 
 __device__ __forceinline__ float finite_or_zero_abs(float x) {
   const float a = fabsf(x);
@@ -57,7 +64,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
     e1 = slot;
     e2 = half_rot + slot;
   }
-  float cs[4], sn[4];
+  float cs[4] = {}, sn[4] = {};
   if (rot) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -69,88 +76,113 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
       sn[u] *= a.rope.attention_factor;
     }
   }
-  bool stored = true;
-  for (int r = r0 + sub; r - sub < r1; r += kRows) {
-    const bool act = r < r1;
-    const int which = r < a.hq ? 0 : (r < a.hq + hkv ? 1 : 2);   // q, k, v
-    const int h = which == 0 ? r : (which == 1 ? r - a.hq : r - a.hq - hkv);
-    const uint16_t* src = which == 0   ? a.q + token * a.q_stride
-                          : which == 1 ? a.k + token * a.k_stride
-                                       : a.v + token * a.v_stride;
-    src += int64_t(h) * D;
-    const int f1 = which == 2 ? 8 * li : e1, f2 = which == 2 ? 8 * li + 4 : e2;
-    uint2 w1 = make_uint2(0u, 0u), w2 = w1;
-    if (act) {
-      w1 = *reinterpret_cast<const uint2*>(src + f1);
-      w2 = *reinterpret_cast<const uint2*>(src + f2);
-    }
-    float x[8];
-    {
-      const float2 p0 = bf16x2_to_float2(w1.x), p1 = bf16x2_to_float2(w1.y);
-      const float2 p2 = bf16x2_to_float2(w2.x), p3 = bf16x2_to_float2(w2.y);
-      x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
-      x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
-    }
-    const bool turn_it = rot && which < 2;
-    if (turn_it) {
-      if (inter) {
+  // cache row of kv-head 0 (-1: no place) and the rows between heads
+  const int64_t row0 = cache_row(a.c, b, 0, pos);
+  const int64_t head_rows = a.c.table != nullptr ? int64_t(kBlock) : a.c.cap;
+  if (row0 < 0 && r1 > a.hq && lane == 0) report(a.status, COBS_ERR_DEVICE);
+  const uint64_t cs2[2] = {pack2(make_float2(cs[0], cs[1])), pack2(make_float2(cs[2], cs[3]))};
+  const uint64_t sn2[2] = {pack2(make_float2(sn[0], sn[1])), pack2(make_float2(sn[2], sn[3]))};
+  const uint64_t ns2[2] = {pack2(make_float2(-sn[0], -sn[1])), pack2(make_float2(-sn[2], -sn[3]))};
+
+  // n head rows of one kind (0 queries, 1 keys, 2 values) from src on; row i
+  // goes to row `row + i step` of dst (and of scales).
+  auto rows = [&](auto kind, const uint16_t* src, int n, void* dst, float* scales, int64_t row,
+                  int64_t step) {
+    constexpr int kKind = decltype(kind)::value;
+    constexpr bool kCode = kKind != 0 && kFormat == COBS_CACHE_E4M3;
+    const bool turn = kKind != 2 && rot;
+    const int f1 = kKind == 2 ? 8 * li : e1, f2 = kKind == 2 ? 8 * li + 4 : e2;
+    for (int rb = sub; rb - sub < n; rb += kBatch * kRows) {
+      uint2 w1[kBatch], w2[kBatch];
+      const uint16_t* p = src + rb * D;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float p = x[2 * u], q = x[2 * u + 1];
-          x[2 * u] = p * cs[u] - q * sn[u];
-          x[2 * u + 1] = q * cs[u] + p * sn[u];
+      for (int i = 0; i < kBatch; ++i) {
+        w1[i] = w2[i] = make_uint2(0u, 0u);
+        if (rb + i * kRows < n) {
+          w1[i] = *reinterpret_cast<const uint2*>(p + i * kRows * D + f1);
+          w2[i] = *reinterpret_cast<const uint2*>(p + i * kRows * D + f2);
         }
-      } else {
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float p = x[u], q = x[4 + u];
-          x[u] = p * cs[u] - q * sn[u];
-          x[4 + u] = q * cs[u] + p * sn[u];
+      for (int i = 0; i < kBatch; ++i) {
+        if (rb - sub + i * kRows >= n) break;    // the same in every lane
+        const bool act = rb + i * kRows < n;
+        if (turn || kCode) {
+          uint64_t x[4] = {pack2(bf16x2_to_float2(w1[i].x)), pack2(bf16x2_to_float2(w1[i].y)),
+                           pack2(bf16x2_to_float2(w2[i].x)), pack2(bf16x2_to_float2(w2[i].y))};
+          if (turn) {
+            if (inter) {   // pairs side by side: x1 of two pairs, x2 of two pairs
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {
+                const float2 m = unpack2(x[u]), q = unpack2(x[u + 1]);
+                x[u] = pack2(make_float2(m.x, q.x));
+                x[u + 1] = pack2(make_float2(m.y, q.y));
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint64_t x1 = inter ? x[2 * u] : x[u], x2 = inter ? x[2 * u + 1] : x[2 + u];
+              const uint64_t y1 = fma2(x2, ns2[u], mul2(x1, cs2[u]));
+              const uint64_t y2 = fma2(x1, sn2[u], mul2(x2, cs2[u]));
+              if (inter) {
+                const float2 m = unpack2(y1), q = unpack2(y2);
+                x[2 * u] = pack2(make_float2(m.x, q.x));
+                x[2 * u + 1] = pack2(make_float2(m.y, q.y));
+              } else {
+                x[u] = y1;
+                x[2 + u] = y2;
+              }
+            }
+          }
+          const float2 v0 = unpack2(x[0]), v1 = unpack2(x[1]), v2 = unpack2(x[2]), v3 = unpack2(x[3]);
+          if constexpr (kCode) {
+            float v[8] = {v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
+            float top = 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top = fmaxf(top, finite_or_zero_abs(v[u]));
+            __syncwarp();
+#pragma unroll
+            for (int m = kLanes / 2; m > 0; m >>= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+            float scale = top / 448.f;
+            if (scale < 1.17549435e-38f) scale = 0.f;
+            const float inv = scale > 0.f ? 1.f / scale : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              v[u] = fabsf(v[u]) <= 3.402823466e38f ? v[u] * inv : __uint_as_float(0x7fffffffu);
+            if (act) {
+              const int64_t r = row + (rb + i * kRows) * step;
+              uint8_t* d = static_cast<uint8_t*>(dst) + r * D;
+              *reinterpret_cast<uint32_t*>(d + f1) = e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16);
+              *reinterpret_cast<uint32_t*>(d + f2) = e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16);
+              if (li == 0) scales[r] = scale;
+            }
+          } else {
+            w1[i] = make_uint2(bf16x2_bits(v0.x, v0.y), bf16x2_bits(v1.x, v1.y));
+            w2[i] = make_uint2(bf16x2_bits(v2.x, v2.y), bf16x2_bits(v3.x, v3.y));
+          }
+        }
+        if (!kCode && act) {
+          uint16_t* d = static_cast<uint16_t*>(dst) + (row + (rb + i * kRows) * step) * D;
+          *reinterpret_cast<uint2*>(d + f1) = w1[i];
+          *reinterpret_cast<uint2*>(d + f2) = w2[i];
         }
       }
     }
-    uint16_t* dst16 = nullptr;
-    int64_t row = 0;
-    if (which == 0) {
-      dst16 = a.q_out + (token * a.hq + h) * int64_t(D);
-    } else {
-      row = cache_row(a.c, b, h, pos);
-      stored &= row >= 0 || !act;
-      dst16 = reinterpret_cast<uint16_t*>(which == 1 ? a.c.k : a.c.v) + row * D;
-    }
-    if (kFormat == COBS_CACHE_E4M3) {
-      float top = 0.f;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) top = fmaxf(top, finite_or_zero_abs(x[u]));
-#pragma unroll
-      for (int m = kLanes / 2; m > 0; m >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      if (which != 0) {
-        float scale = top / 448.f;
-        if (scale < 1.17549435e-38f) scale = 0.f;
-        const float inv = scale > 0.f ? 1.f / scale : 0.f;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          x[u] = fabsf(x[u]) <= 3.402823466e38f ? x[u] * inv : __uint_as_float(0x7fffffffu);
-        if (act && row >= 0) {
-          uint8_t* dst = reinterpret_cast<uint8_t*>(which == 1 ? a.c.k : a.c.v) + row * D;
-          *reinterpret_cast<uint32_t*>(dst + f1) = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
-          *reinterpret_cast<uint32_t*>(dst + f2) = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
-          if (li == 0) (which == 1 ? a.c.ks : a.c.vs)[row] = scale;
-        }
-        continue;
-      }
-    }
-    if (act && (which == 0 || row >= 0)) {
-      if (turn_it) {
-        w1 = make_uint2(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]));
-        w2 = make_uint2(bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7]));
-      }
-      *reinterpret_cast<uint2*>(dst16 + f1) = w1;
-      *reinterpret_cast<uint2*>(dst16 + f2) = w2;
-    }
-  }
-  if (!stored) report(a.status, COBS_ERR_DEVICE);
+  };
+  const int q1 = min(r1, a.hq);
+  if (r0 < q1)
+    rows(Kind<0>(), a.q + token * a.q_stride + r0 * D, q1 - r0, a.q_out, nullptr,
+         token * a.hq + r0, 1);
+  if (row0 < 0) return;
+  const int k0 = max(r0 - a.hq, 0), k1 = min(r1 - a.hq, hkv);
+  if (k0 < k1)
+    rows(Kind<1>(), a.k + token * a.k_stride + k0 * D, k1 - k0, a.c.k, a.c.ks,
+         row0 + k0 * head_rows, head_rows);
+  const int v0 = max(r0 - a.hq - hkv, 0), v1 = min(r1 - a.hq - hkv, hkv);
+  if (v0 < v1)
+    rows(Kind<2>(), a.v + token * a.v_stride + v0 * D, v1 - v0, a.c.v, a.c.vs,
+         row0 + v0 * head_rows, head_rows);
 }
 
 }  // namespace
@@ -158,7 +190,13 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
 cudaError_t launch_append(const AppendArgs& a0, cudaStream_t stream) {
   AppendArgs a = a0;
   const int n_rows = a.hq + 2 * a.c.hkv;
-  a.rows_per_warp = 8;
+  // Few tokens: a pass of one row per sub-warp, so that the GPU is filled and
+  // nothing waits in turn; many: up to kBatch loads' worth four times over, so
+  // that the sines are shared.  About 32 warps per SM lie between the two.
+  const int per_pass = 32 / (a.d / 8);
+  int64_t rows = a.n_tokens * n_rows / (int64_t(148) * 32);
+  rows = rows < per_pass ? per_pass : (rows > 4 * kBatch * per_pass ? 4 * kBatch * per_pass : rows);
+  a.rows_per_warp = int32_t(rows / per_pass * per_pass);
   a.chunks = (n_rows + a.rows_per_warp - 1) / a.rows_per_warp;
   const int64_t ctas = (a.n_tokens * a.chunks + kAppendWarps - 1) / kAppendWarps;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;

@@ -64,6 +64,23 @@ __device__ __forceinline__ bool wait_step(uint64_t* bar, uint32_t parity, int32_
   return true;
 }
 
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Two fp32 -> packed bf16 (low half: x), nearest even, NaN kept.
 __device__ __forceinline__ uint32_t bf16x2_bits(float x, float y) {
   uint32_t r;

@@ -32,31 +32,54 @@ __global__ void __launch_bounds__(kReadThreads) read_cache_kernel(const ReadArgs
     if (page < 0) return;
     row0 = (int64_t(page) * a.c.hkv + h) * kBlock;
   }
-  const int li = threadIdx.x % kLanes;
+  // all loads of K and V first, then the conversions and stores
+  constexpr int kStep = kReadThreads / kLanes, kPer = kBlock / kStep;
+  const int li = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
+  uint4 w[2][kPer];
+  float sc[2][kPer];
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const void* src = which ? a.c.v : a.c.k;
+    const float* scales = which ? a.c.vs : a.c.ks;
+    const bool wanted = (which ? a.v_out : a.k_out) != nullptr;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = r0 + i * kStep;
+      w[which][i] = make_uint4(0u, 0u, 0u, 0u);
+      sc[which][i] = 0.f;
+      if (!wanted || r >= rows) continue;
+      const int64_t at = (row0 + r) * D + 8 * li;
+      if (kFormat == COBS_CACHE_BF16) {
+        w[which][i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at));
+      } else {
+        const uint2 c = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(src) + at));
+        w[which][i].x = c.x;
+        w[which][i].y = c.y;
+        sc[which][i] = __ldg(scales + row0 + r);
+      }
+    }
+  }
+#pragma unroll
   for (int which = 0; which < 2; ++which) {
     uint16_t* out = which ? a.v_out : a.k_out;
     if (out == nullptr) continue;
-    const void* src = which ? a.c.v : a.c.k;
-    const float* scales = which ? a.c.vs : a.c.ks;
-    for (int r = threadIdx.x / kLanes; r < rows; r += kReadThreads / kLanes) {
-      uint4 w;
-      if (kFormat == COBS_CACHE_BF16) {
-        w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) +
-                                            (row0 + r) * D + 8 * li);
-      } else {
-        const uint2 codes = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(src) +
-                                                            (row0 + r) * D + 8 * li);
-        const float sc = scales[row0 + r];
-        const uint32_t c[4] = {codes.x & 0xffffu, codes.x >> 16, codes.y & 0xffffu, codes.y >> 16};
-        uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = r0 + i * kStep;
+      if (r >= rows) continue;
+      uint4 o = w[which][i];
+      if (kFormat == COBS_CACHE_E4M3) {
+        const float s = sc[which][i];
+        const uint32_t c[4] = {o.x & 0xffffu, o.x >> 16, o.y & 0xffffu, o.y >> 16};
+        uint32_t v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float2 f = e4m3x2_to_float2(c[u]);
-          o[u] = bf16x2_bits(f.x * sc, f.y * sc);
+          v[u] = bf16x2_bits(f.x * s, f.y * s);
         }
-        w = make_uint4(o[0], o[1], o[2], o[3]);
+        o = make_uint4(v[0], v[1], v[2], v[3]);
       }
-      *reinterpret_cast<uint4*>(out + ((page_out * a.c.hkv + h) * kBlock + r) * D + 8 * li) = w;
+      *reinterpret_cast<uint4*>(out + ((page_out * a.c.hkv + h) * kBlock + r) * D + 8 * li) = o;
     }
   }
 }

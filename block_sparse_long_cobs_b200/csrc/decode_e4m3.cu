@@ -206,18 +206,25 @@ decode_e4m3_kernel(const __grid_constant__ CUtensorMap kmap,
           }
           break;
         }
+        // the blocks of the next tile are asked for one tile ahead, those of the
+        // first together with the count
+        const int s0 = int(c % a.chunks_per_pair) * a.chunk_slots;
+        const int32_t* row = a.idx + (c / a.chunks_per_pair) * a.idx_stride + s0;
+        int jn[2] = {__ldg(row), s0 + 1 < a.idx_stride ? __ldg(row + 1) : -1};
         const Chunk g = chunk_of(c, a);
         const int64_t b = g.pair / a.hkv;
         const int64_t len_b =
             kMode == 0 ? a.seq_len : sequence_length(a.seq_lens, a.seq_len, b, a.status, false);
         const int64_t blocks_b = kMode == 0 ? seq_blocks : (len_b + kBlock - 1) / kBlock;
-        const int32_t* row = a.idx + g.pair * a.idx_stride + g.s0;
         for (int t = 0; 2 * t < g.nb && ok; ++t, ++gt) {
           const int nh = 2 * t + 1 < g.nb ? 2 : 1;
+          const int jc[2] = {jn[0], jn[1]};
+          if (2 * t + 2 < g.nb) jn[0] = __ldg(row + 2 * t + 2);
+          if (2 * t + 3 < g.nb) jn[1] = __ldg(row + 2 * t + 3);
           int y[2] = {0, 0}, z[2] = {0, 0};
           int64_t r0[2] = {-1, -1};       // first row of the block's scales
           for (int h2 = 0; h2 < nh; ++h2) {
-            const int j = __ldg(row + 2 * t + h2);
+            const int j = jc[h2];
             bool in = j >= 0 && j < blocks_b;
             if constexpr (kMode == 2) {
               const int32_t page = in ? __ldg(a.block_table + b * a.table_stride + j) : -1;
