@@ -69,6 +69,26 @@ cobs_status check_rows(const char* name, const void* p, int64_t stride, int64_t 
   return COBS_OK;
 }
 
+// Whether p is memory of the current device, or memory that it can reach: the
+// last check before a launch (a host pointer, or another device's, would
+// fault in the kernel).
+cobs_status check_device(const char* name, const void* p) {
+  int dev = 0;
+  cudaPointerAttributes at{};
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, p);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();   // not sticky: leave no error behind
+    return fail(COBS_ERR_INVALID_ARG, "%s is not a device pointer", name);
+  }
+  if (at.type == cudaMemoryTypeUnregistered)
+    return fail(COBS_ERR_INVALID_ARG, "%s is not a device pointer", name);
+  if (at.type == cudaMemoryTypeDevice && at.device != dev)
+    return fail(COBS_ERR_INVALID_ARG, "%s lies on device %d, the current device is %d", name,
+                at.device, dev);
+  return COBS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -159,6 +179,8 @@ cobs_status cobs_append_tokens(const cobs_dims* dims, const cobs_kv_cache* cache
   }
   if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != COBS_OK) return st;
   if (n_tokens == 0) return ok();
+  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
+  if ((st = check_device("k", k)) != COBS_OK) return st;
   AppendArgs a{};
   a.c = view_of(dims, cache);
   if (rope) a.rope = *rope;
@@ -197,6 +219,8 @@ cobs_status cobs_read_cache(const cobs_dims* dims, const cobs_kv_cache* cache,
     return fail(COBS_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
   if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != COBS_OK) return st;
   if (block_end == block_begin) return ok();
+  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
+  if ((st = check_device("k_out or v_out", k_out ? k_out : v_out)) != COBS_OK) return st;
   ReadArgs a{};
   a.c = view_of(dims, cache);
   a.seq_lens = seq_lens;
@@ -253,6 +277,8 @@ cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_cache* ca
   const size_t need = kStatusBytes + prompt_partial_bytes(dims, n_tokens, max_seq_len);
   if ((st = check_ws(ws, ws_bytes, need)) != COBS_OK) return st;
   if (n_tokens == 0) return ok();
+  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
+  if ((st = check_device("q", q)) != COBS_OK) return st;
   PromptArgs a{};
   a.c = view_of(dims, cache);
   a.q = static_cast<const uint16_t*>(q);
@@ -289,6 +315,8 @@ cobs_status cobs_sparse_decode_cache(const cobs_dims* dims, const cobs_kv_cache*
                    cache->n_pages, idx, n_sel, idx_stride, seq_lens, max_seq_len, softmax_scale,
                    out, lse, ws, ws_bytes, &a);
   if (st != COBS_OK) return st;
+  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
+  if ((st = check_device("q", q)) != COBS_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->format == COBS_CACHE_BF16
                             ? launch_decode(a, s)

@@ -1,0 +1,197 @@
+"""The cache and prompt calls in a row, as a server makes them: prompts of
+different lengths appended in chunks, the chunks' attention, the statistics of
+the blocks that became complete, then decode steps (append one token, select,
+decode), over a bf16 cache and over an E4M3 cache whose chunks are read back
+as pages.  Every result is checked against the softmax in 64 bits over what
+the cache holds, and the cache's keys against the rotated projections."""
+
+import itertools
+import math
+
+import pytest
+import torch
+
+import block_sparse_long_cobs_b200 as cb
+from cache_ref import B, attend, bf16_rows, cu_of, frequencies, ints, page_table, rotate, workspace
+
+pytestmark = pytest.mark.gpu
+
+HQ, HKV, D, RANK = 8, 2, 128, 4
+G = HQ // HKV
+SCALE = 1.0 / math.sqrt(D)
+
+
+class Server:
+    def __init__(self, lens, cap, e4m3, paged, seed=7):
+        self.g = torch.Generator(device="cuda")
+        self.g.manual_seed(seed)
+        self.batch, self.cap, self.e4m3, self.paged = len(lens), cap, e4m3, paged
+        nb = cap // B
+        self.table = None
+        shape = (self.batch, HKV, cap)
+        if paged:
+            self.table, n_pages = page_table(self.g, [nb] * self.batch, spare=2, width_pad=0)
+            shape = (n_pages, HKV, B)
+        kind = torch.uint8 if e4m3 else torch.bfloat16
+        # unused rows: a NaN code, or NaN
+        self.k = torch.full(shape + (D,), 0x7F if e4m3 else float("nan"), dtype=kind, device="cuda")
+        self.v = self.k.clone()
+        self.ks = torch.full(shape, float("nan"), device="cuda") if e4m3 else None
+        self.vs = self.ks.clone() if e4m3 else None
+        self.cache = cb.cobs_kv_cache(self.k, self.v, self.ks, self.vs, self.table,
+                                      shape[0] if paged else 0, nb if paged else 0, int(e4m3))
+        self.dims = cb.cobs_dims(batch=self.batch, num_q_heads=HQ, num_kv_heads=HKV, head_dim=D,
+                                 block_size=B, rank=RANK, capacity_tokens=cap)
+        self.rope = cb.cobs_rope_init(64, False, scaling=cb.COBS_ROPE_LINEAR, factor=2.0)
+        self.f = frequencies(64, scaling=cb.COBS_ROPE_LINEAR, factor=2.0)
+        self.lens = [0] * self.batch
+        self.stats = torch.zeros(self.batch, HKV, nb, (1 + RANK) * D, dtype=torch.bfloat16,
+                                 device="cuda")
+        self.ws = workspace(cb.cobs_prompt_workspace_bytes(self.dims, 512, cap))
+        self.top_k, self.sink, self.local = 4, 1, 64
+        self.stride = cb.cobs_selected_capacity(self.dims, self.top_k, self.sink, self.local)
+        self.dws = workspace(cb.cobs_workspace_bytes(self.dims, self.top_k, self.sink, self.local))
+        self.want_k = [[] for _ in range(self.batch)]      # rotated keys in 64 bits
+        # pages of the read-back cache: block j of sequence b is page b * nb + j
+        self.pages = torch.full((self.batch * nb, HKV, B, D), float("nan"), dtype=torch.bfloat16,
+                                device="cuda")
+        self.vpages = self.pages.clone()
+        self.ptable = torch.arange(self.batch * nb, dtype=torch.int32, device="cuda").view(
+            self.batch, nb)
+
+    def rows(self, name, b, h):
+        n = self.lens[b]
+        x = {"k": (self.k, self.ks), "v": (self.v, self.vs)}[name]
+
+        def get(t):
+            if self.table is None:
+                return t[b, h, :n]
+            return t[self.table[b].long(), h].flatten(0, 1)[:n]
+        if self.e4m3:
+            return get(x[0]).contiguous().view(torch.float8_e4m3fn).double() * \
+                get(x[1]).double()[:, None]
+        return get(x[0]).double()
+
+    def append(self, counts):
+        n = sum(counts)
+        qkv = bf16_rows(self.g, n, HQ + 2 * HKV, D, scale=1.5)
+        q_out = torch.empty(n, HQ, D, dtype=torch.bfloat16, device="cuda")
+        wide = (HQ + 2 * HKV) * D
+        one = all(c == 1 for c in counts)
+        cb.cobs_append_tokens(self.dims, self.cache, self.rope, qkv[:, :HQ], wide,
+                              qkv[:, HQ:HQ + HKV], wide, qkv[:, HQ + HKV:], wide,
+                              None if one else cu_of(counts), n, ints(self.lens), q_out, self.ws,
+                              self.ws.numel())
+        first = 0
+        for b, c in enumerate(counts):
+            pos = torch.arange(self.lens[b], self.lens[b] + c, device="cuda")
+            x = qkv[first:first + c, HQ:HQ + HKV].double()
+            self.want_k[b].append(rotate(x, pos, self.f, False)[0])
+            self.lens[b] += c
+            first += c
+        return q_out
+
+    def bf16_cache(self):
+        """The cache that statistics and prompt attention read."""
+        if not self.e4m3:
+            return self.cache
+        nb = self.cap // B
+        cb.cobs_read_cache(self.dims, self.cache, ints(self.lens), 0, nb, self.pages, self.vpages,
+                           self.ws, self.ws.numel())
+        return cb.cobs_kv_cache(self.pages, self.vpages, None, None, self.ptable, self.batch * nb,
+                                nb, cb.COBS_CACHE_BF16)
+
+    def prompt(self, counts):
+        q = self.append(counts)
+        cache = self.bf16_cache()
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:2], device="cuda")
+        cb.cobs_prompt_attention(self.dims, cache, q, cu_of(counts), q.shape[0], ints(self.lens),
+                                 max(self.lens), SCALE, out, lse, self.ws, self.ws.numel())
+        first = 0
+        for b, c in enumerate(counts):
+            for h in range(HKV if c else 0):
+                k, v = self.rows("k", b, h), self.rows("v", b, h)
+                if self.e4m3:
+                    k, v = k.float().bfloat16().double(), v.float().bfloat16().double()
+                for i, g in itertools.product((0, c // 2, c - 1), range(G)):
+                    n = self.lens[b] - c + i + 1
+                    qr = q[first + i, h * G + g].double()[None]
+                    want, wl, w = attend(qr, k[:n], v[:n], SCALE)
+                    got = out[first + i, h * G + g].double()
+                    assert ((got - want[0]).abs() <= 2.0 ** -8 * want[0].abs()
+                            + 2.0 ** -7 * w[0]).all()
+                    assert abs(float(lse[first + i, h * G + g] - wl[0])) <= 2.0 ** -10
+            first += c
+        # statistics of every block that is complete by now
+        done = min(self.lens) // B
+        src = cache
+        if src.block_table:
+            pool, tab = (self.pages, self.ptable) if self.e4m3 else (self.k, self.table)
+            cb.cobs_build_block_stats_paged(self.dims, pool, pool.shape[0], tab, tab.shape[1], 0,
+                                            done, self.stats, self.ws, self.ws.numel())
+        else:
+            cb.cobs_build_block_stats(self.dims, self.k, 0, done, self.stats, self.ws,
+                                      self.ws.numel())
+
+    def decode(self):
+        q = self.append([1] * self.batch)
+        idx = torch.full((self.batch, HKV, self.stride), -5, dtype=torch.int32, device="cuda")
+        n_sel = torch.zeros(self.batch, HKV, dtype=torch.int32, device="cuda")
+        out = torch.empty(self.batch, HQ, D, device="cuda")
+        lse = torch.empty(self.batch, HQ, device="cuda")
+        lens, most = ints(self.lens), max(self.lens)
+        cb.cobs_select_blocks_varlen(self.dims, q, self.stats, lens, most, self.top_k, self.sink,
+                                     self.local, idx, self.stride, n_sel, None, self.dws,
+                                     self.dws.numel())
+        cb.cobs_sparse_decode_cache(self.dims, self.cache, q, idx, n_sel, self.stride, lens, most,
+                                    SCALE, out, lse, self.dws, self.dws.numel())
+        for b, h in itertools.product(range(self.batch), range(HKV)):
+            blocks = idx[b, h, :int(n_sel[b, h])].tolist()
+            n = self.lens[b]
+            assert 0 in blocks and (n - 1) // B in blocks and blocks == sorted(set(blocks))
+            at = torch.cat([torch.arange(j * B, min(n, j * B + B), device="cuda") for j in blocks])
+            k, v = self.rows("k", b, h)[at], self.rows("v", b, h)[at]
+            want, wl, w = attend(q[b, h * G:(h + 1) * G].double(), k, v, SCALE)
+            got = out[b, h * G:(h + 1) * G].double()
+            assert ((got - want).abs() <= 2.0 ** -13 * w + 2.0 ** -16).all()
+            assert ((lse[b, h * G:(h + 1) * G].double() - wl).abs() <= 2.0 ** -13).all()
+
+    def finish(self):
+        assert cb.cobs_read_device_status(self.ws, self.ws.numel()) == 0
+        assert cb.cobs_read_device_status(self.dws, self.dws.numel()) == 0
+        for b, h in itertools.product(range(self.batch), range(HKV)):
+            want = torch.cat(self.want_k[b])[:, h]
+            got = self.rows("k", b, h)
+            step = 2.0 ** -4 if self.e4m3 else 2.0 ** -8
+            top = want.abs().amax(-1, keepdim=True)
+            assert ((got - want).abs() <= step * want.abs() + 2.0 ** -18 * top).all()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_prompt_in_chunks_then_decode(e4m3, paged):
+    s = Server([0, 0, 0], 1024, e4m3, paged)
+    s.prompt([300, 129, 200])
+    s.prompt([1, 70, 0])
+    s.prompt([256, 100, 64])
+    for _ in range(3):
+        s.decode()
+    s.prompt([5, 60, 130])
+    s.decode()
+    s.finish()
+
+
+def test_wrong_memory_is_refused():
+    """A host address where device memory is needed."""
+    s = Server([0], 128, False, False)
+    host = torch.zeros(4, HQ, D, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        cb.cobs_prompt_attention(s.dims, s.cache, host, cu_of([4]), 4, ints([4]), 64, SCALE,
+                                 torch.zeros(4, HQ, D, device="cuda"), None, s.ws, s.ws.numel())
+    with pytest.raises(cb.CobsError) as e:
+        cb.cobs_prompt_attention(s.dims, s.cache, host.data_ptr() & ~15, cu_of([4]), 4, ints([4]),
+                                 64, SCALE, torch.zeros(4, HQ, D, dtype=torch.bfloat16,
+                                                        device="cuda"), None, s.ws, s.ws.numel())
+    assert e.value.status == cb.COBS_ERR_INVALID_ARG
+    assert "device pointer" in cb.cobs_last_error()
