@@ -162,6 +162,19 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   return v;
 }
 
+// 16-byte units x (first) and y (second) of a pair: lanes with `bit` clear keep
+// x and give y for the partner's x, lanes with it set the other way round.
+__device__ __forceinline__ void swap_units(uint4& x, uint4& y, int lane, int bit) {
+  const bool up = (lane & bit) != 0;
+  uint4 s = up ? x : y;
+  s.x = __shfl_xor_sync(0xffffffffu, s.x, bit);
+  s.y = __shfl_xor_sync(0xffffffffu, s.y, bit);
+  s.z = __shfl_xor_sync(0xffffffffu, s.z, bit);
+  s.w = __shfl_xor_sync(0xffffffffu, s.w, bit);
+  if (up) x = s;
+  else y = s;
+}
+
 // A CTA's share of the work: where it starts and how much it is (units when
 // `whole`, else iterations).
 struct Share {
@@ -303,8 +316,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane
-  const int group = a.hq / a.c.hkv;
-  const int tt = kTileRows / group;        // tokens of a tile
+  const int group = a.hq / a.c.hkv;        // 1, 2, 4 or 8
+  const int gs = __ffs(group) - 1;
+  const int tt = kTileRows >> gs;          // tokens of a tile
 
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
@@ -659,8 +673,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // two tiles: each warpgroup has one; one tile: both have its rows, and
       // every second iteration
       const bool two = seg_q[qs].ntok > tt;
-      const int tok = (two ? w * tt : 0) + row / group;   // token of the unit
-      const int tok_w = (two ? w * tt : 0) + (warp & 3) * 32 / group;   // the warp's first
+      const int tok = (two ? w * tt : 0) + (row >> gs);   // token of the unit
+      const int tok_w = (two ? w * tt : 0) + ((warp & 3) * 32 >> gs);   // the warp's first
       const bool busy = tok_w < seg_q[qs].ntok;   // a row of the warp is a token's
       const int it0 = seg_q[qs].it0, it1 = seg_q[qs].it1;
       const int pos = int(seg_q[qs].pos0) + tok;
@@ -733,31 +747,32 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[w][half]);
           };
+          // The first half with the maximum as it was: it moves so rarely that
+          // the weights are formed while the new one is still being found, and
+          // again in the case that it did move.  (One copy of the code for
+          // every case: what runs once a unit comes from a cold instruction
+          // cache.)
           float sum;
-          if (i == first) {
-            m = row_max();
+          bool sure = i == first;
+          if (sure) m = row_max();
+          for (;;) {
             sum = weights(0);
-          } else {
-            // The first half with the maximum as it was: it moves so rarely
-            // that the weights are formed while the new one is still being
-            // found, and again in the case that it did move.
-            sum = weights(0);
+            if (sure) break;
             const float mx = row_max();
             const bool raise = mx > m + kRescaleLog2;
-            if (__any_sync(0xffffffffu, raise)) {
-              const float mn = raise ? mx : m;
-              const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
-              m = mn;
-              l *= alpha;
+            sure = __any_sync(0xffffffffu, raise);
+            if (!sure) break;
+            const float mn = raise ? mx : m;
+            const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
+            m = mn;
+            l *= alpha;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {   // narrow: 128 scores are live
+              float o[16];
+              tmem_ld16(o_addr + c, o);
 #pragma unroll
-              for (int c = 0; c < D; c += 16) {   // narrow: 128 scores are live
-                float o[16];
-                tmem_ld16(o_addr + c, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                tmem_st16(o_addr + c, reinterpret_cast<const uint32_t*>(o));
-              }
-              sum = weights(0);
+              for (int e = 0; e < 16; ++e) o[e] *= alpha;
+              tmem_st16(o_addr + c, reinterpret_cast<const uint32_t*>(o));
             }
           }
           release(0);
@@ -794,7 +809,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // (read again: nothing but the loop's own state stays in registers)
         const int type = seg_q[qs].type;
         const int64_t tok0 = seg_q[qs].tok0;
-        const bool mine = tok < seg_q[qs].ntok;
+        const int ntok = seg_q[qs].ntok, head0 = seg_q[qs].h * group;
+        const bool mine = tok < ntok;
         const float mm = fmaxf(m, m1);
         const bool some = mm != -INFINITY;           // the row has a key
         const float w0 = m != -INFINITY ? hw_exp2(m - mm) : 0.f;
@@ -802,13 +818,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const float ll = l * w0 + l1 * w1;
         const float inv = type == kWhole ? (some ? 1.f / ll : 0.f) : 1.f;
         const float f0 = w0 * inv, f1 = w1 * inv;
-        const int64_t r = (tok0 + tok) * a.hq + seg_q[qs].h * group + row % group;
+        const int64_t r = (tok0 + tok) * a.hq + head0 + (row & (group - 1));
         float* part = slot_rows(a, D, 2 * int64_t(blockIdx.x) + (type == kBegin ? 1 : 0));
         const int pr = (two ? w * kTileRows : 0) + row;
         // (not from f1 alone: rows of nobody may hold NaN, and the second tile
         // has no columns after its own)
         const bool both = !two && __any_sync(0xffffffffu, m1 != -INFINITY);
-#pragma unroll
+        // (not unrolled: four copies of this, run once a unit from a cold
+        // instruction cache, took 9000 cycles)
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           __syncwarp();   // rows of nobody skip the stores: together again for the load
@@ -821,14 +839,30 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = f1 != 0.f ? fmaf(o1[e], f1, o[e]) : o[e];
           }
-          if (mine && type == kWhole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + r * D + c);
+          if (type == kWhole) {
+            // 32 columns of 4 rows in 4 lanes, transposed in units of 16
+            // bytes: each store then covers 64 bytes of 8 rows instead of 16
+            // bytes of 32
+            uint4 p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(bf16x2_bits(o[8 * e], o[8 * e + 1]),
-                                  bf16x2_bits(o[8 * e + 2], o[8 * e + 3]),
-                                  bf16x2_bits(o[8 * e + 4], o[8 * e + 5]),
-                                  bf16x2_bits(o[8 * e + 6], o[8 * e + 7]));
+              p[e] = make_uint4(bf16x2_bits(o[8 * e], o[8 * e + 1]),
+                                bf16x2_bits(o[8 * e + 2], o[8 * e + 3]),
+                                bf16x2_bits(o[8 * e + 4], o[8 * e + 5]),
+                                bf16x2_bits(o[8 * e + 6], o[8 * e + 7]));
+            swap_units(p[0], p[1], lane, 1);
+            swap_units(p[2], p[3], lane, 1);
+            swap_units(p[0], p[2], lane, 2);
+            swap_units(p[1], p[3], lane, 2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int rr = (row & ~3) + e;     // the row of p[e] now
+              const int tr = (two ? w * tt : 0) + (rr >> gs);
+              if (tr < ntok)
+                *reinterpret_cast<uint4*>(
+                    a.out + ((tok0 + tr) * a.hq + head0 + (rr & (group - 1))) * D + c + 8 * (lane & 3)) =
+                    p[e];
+            }
           } else if (mine) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -859,56 +893,79 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
 // Units that were cut, joined: the CTA whose last segment begins a unit
 // (slot 1) and the following CTAs' first segments (slot 0) up to the one that
-// ends it.  Block (c, y) joins 16 dimensions of the unit that begins in
-// CTA c, one row per thread:
+// ends it.  Block (c, y) joins 8 dimensions of the unit that begins in CTA c,
+// one row per thread, the loads of 4 segments at a time:
 //   M = max m_s, L = sum 2^(m_s - M) l_s, out = sum 2^(m_s - M) o_s / L.
-constexpr int kMergeDims = 16;
+// (One segment after the other it took 28 us for 19 segments of 128 rows.)
+constexpr int kMergeDims = 8;
+constexpr int kMergeBatch = 4;
 template <int D>
 __global__ void __launch_bounds__(kUnitRows) prompt_merge_kernel(const PromptArgs a, int n_ctas) {
+  __shared__ int n_follow;
   pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x;
   const SlotNote g = *slot_note(a, 2 * int64_t(c) + 1);
   if (g.type != kBegin) return;
+  const int r = threadIdx.x;
+  // segments that follow the first: up to the first one that ends a unit
+  if (r == 0) n_follow = n_ctas - 1 - c;
+  __syncthreads();
+  if (c + 1 + r < n_ctas && slot_note(a, 2 * int64_t(c + 1 + r))->type == kEnd)
+    atomicMin(&n_follow, r + 1);
+  __syncthreads();
+  const int n_seg = 1 + n_follow;
   const int group = a.hq / a.c.hkv;
   const int tt = kTileRows / group;
-  const int r = threadIdx.x;
   const int tok = r / kTileRows * tt + r % kTileRows / group;
   if (tok >= g.ntok) return;
   const int d0 = blockIdx.y * kMergeDims;
   float M = -INFINITY, L = 0.f, o[kMergeDims] = {};
-  int type = kBegin;
-  for (int s = c; s < n_ctas && type != kEnd; ++s) {
-    const int64_t slot = 2 * int64_t(s) + (s == c ? 1 : 0);
-    type = s == c ? int(kBegin) : slot_note(a, slot)->type;
-    const float* part = slot_rows(a, D, slot);
-    const float m = __ldcg(part + kUnitRows * D + r), l = __ldcg(part + kUnitRows * (D + 1) + r);
-    float4 v[kMergeDims / 4];
+  for (int s0 = 0; s0 < n_seg; s0 += kMergeBatch) {
+    float m[kMergeBatch], l[kMergeBatch], top = M;
+    float4 v[kMergeBatch][kMergeDims / 4];
 #pragma unroll
-    for (int e = 0; e < kMergeDims / 4; ++e)
-      v[e] = __ldcg(reinterpret_cast<const float4*>(part) + (d0 / 4 + e) * kUnitRows + r);
-    if (m == -INFINITY) continue;
-    const float mn = fmaxf(M, m);
-    const float wo = hw_exp2(M - mn), wn = hw_exp2(m - mn);   // 2^-inf = 0
-    L = L * wo + l * wn;
+    for (int i = 0; i < kMergeBatch; ++i) {
+      const int s = s0 + i;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < kMergeDims / 4; ++e) {
-      o[4 * e] = o[4 * e] * wo + v[e].x * wn;
-      o[4 * e + 1] = o[4 * e + 1] * wo + v[e].y * wn;
-      o[4 * e + 2] = o[4 * e + 2] * wo + v[e].z * wn;
-      o[4 * e + 3] = o[4 * e + 3] * wo + v[e].w * wn;
+      for (int e = 0; e < kMergeDims / 4; ++e) v[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < n_seg) {
+        const float* part = slot_rows(a, D, 2 * int64_t(c + s) + (s == 0 ? 1 : 0));
+        m[i] = __ldcg(part + kUnitRows * D + r);
+        l[i] = __ldcg(part + kUnitRows * (D + 1) + r);
+#pragma unroll
+        for (int e = 0; e < kMergeDims / 4; ++e)
+          v[i][e] = __ldcg(reinterpret_cast<const float4*>(part) + (d0 / 4 + e) * kUnitRows + r);
+      }
+      top = fmaxf(top, m[i]);
     }
-    M = mn;
+    if (top == -INFINITY) continue;
+    const float f = hw_exp2(M - top);   // 2^-inf = 0
+    M = top;
+    L *= f;
+#pragma unroll
+    for (int e = 0; e < kMergeDims; ++e) o[e] *= f;
+#pragma unroll
+    for (int i = 0; i < kMergeBatch; ++i) {
+      if (m[i] == -INFINITY) continue;
+      const float w = hw_exp2(m[i] - M);
+      L = fmaf(w, l[i], L);
+#pragma unroll
+      for (int e = 0; e < kMergeDims / 4; ++e) {
+        o[4 * e] = fmaf(w, v[i][e].x, o[4 * e]);
+        o[4 * e + 1] = fmaf(w, v[i][e].y, o[4 * e + 1]);
+        o[4 * e + 2] = fmaf(w, v[i][e].z, o[4 * e + 2]);
+        o[4 * e + 3] = fmaf(w, v[i][e].w, o[4 * e + 3]);
+      }
+    }
   }
   const int64_t row = (g.tok0 + tok) * a.hq + g.h * group + r % group;
   const float inv = M != -INFINITY ? 1.f / L : 0.f;
-  uint32_t out[kMergeDims / 2];
-#pragma unroll
-  for (int e = 0; e < kMergeDims / 2; ++e) out[e] = bf16x2_bits(o[2 * e] * inv, o[2 * e + 1] * inv);
-#pragma unroll
-  for (int e = 0; e < kMergeDims / 8; ++e)
-    reinterpret_cast<uint4*>(a.out + row * D + d0)[e] =
-        make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
+  *reinterpret_cast<uint4*>(a.out + row * D + d0) =
+      make_uint4(bf16x2_bits(o[0] * inv, o[1] * inv), bf16x2_bits(o[2] * inv, o[3] * inv),
+                 bf16x2_bits(o[4] * inv, o[5] * inv), bf16x2_bits(o[6] * inv, o[7] * inv));
   if (blockIdx.y == 0 && a.lse != nullptr)
     a.lse[row] = M != -INFINITY ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
