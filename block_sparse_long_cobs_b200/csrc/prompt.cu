@@ -804,12 +804,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         m1 = other_ml[0][row];
         l1 = other_ml[1][row];
       }
+      // (read again: nothing but the loop's own state stays in registers; given
+      // back before the stores, which an arrival would wait for)
+      const int type = seg_q[qs].type;
+      const int64_t tok0 = seg_q[qs].tok0;
+      const int ntok = seg_q[qs].ntok, head0 = seg_q[qs].h * group;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[qs]);
       if (busy && (two || w == 0)) {
         tc_fence_after();
-        // (read again: nothing but the loop's own state stays in registers)
-        const int type = seg_q[qs].type;
-        const int64_t tok0 = seg_q[qs].tok0;
-        const int ntok = seg_q[qs].ntok, head0 = seg_q[qs].h * group;
         const bool mine = tok < ntok;
         const float mm = fmaxf(m, m1);
         const bool some = mm != -INFINITY;           // the row has a key
@@ -879,10 +882,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) {
-        if (!two && w == 0) mbar_arrive(&ml_free);
-        mbar_arrive(&seg_empty[qs]);
-      }
+      if (!two && w == 0 && lane == 0) mbar_arrive(&ml_free);
       joins += two ? 0u : 1u;
     }
   }
