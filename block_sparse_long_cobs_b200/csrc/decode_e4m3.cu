@@ -461,8 +461,8 @@ decode_e4m3_kernel(const __grid_constant__ CUtensorMap kmap,
         const float f = pM[h] == -INFINITY ? 0.f : hw_exp2(pM[h] - pm[h]);
         const float ov = f > 0.f ? o[h] * f : 0.f;
         if (a.chunks_per_pair == 1) {
-          if (r < a.d) a.out[(hq0 + h) * a.d + r] = l > 0.f ? ov / l : 0.f;
-          if (r == h) a.lse[hq0 + h] = l > 0.f ? (pm[h] + log2f(l)) * kLn2 : -INFINITY;
+          if (r < a.d) a.out[(hq0 + h) * a.d + r] = l != 0.f ? ov / l : 0.f;
+          if (r == h) a.lse[hq0 + h] = l != 0.f ? (pm[h] + log2f(l)) * kLn2 : -INFINITY;
         } else {
           float* part = a.partials + (hq0 + h) * hstride + int64_t(pg.seg) * (a.d + 2);
           if (r < a.d) part[r] = ov;

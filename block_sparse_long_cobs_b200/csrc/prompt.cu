@@ -11,17 +11,31 @@
 // tokens of one sequence and kv-head) against all keys up to the unit's last
 // position, 128 keys per iteration.  Per iteration and tile the tensor cores
 // form S = Q K^T (M = 128 rows, N = 128 keys) and O += P V (P read from
-// tensor memory).  The two tiles alternate: while one tile's P is formed the
-// tensor cores work for the other, so that neither waits.
-//   warps 0-3, 4-7  softmax of tile 0, 1: one row per thread.  p = 2^(s - m)
-//                   with m raised only when a row's logit exceeds it by more
-//                   than 2^8 (the warp then rescales its rows of O in tensor
-//                   memory; the products that wrote them were issued before
-//                   the ones that made S, so they are complete).  P
+// tensor memory, half a tile as soon as its weights are there).  The two tiles
+// alternate: while one tile's P is formed the tensor cores work for the other.
+// A unit of one tile (few rows) gives its even iterations to one softmax
+// warpgroup and its odd ones to the other, each with its own S, O, m and l,
+// joined at the end.
+//   warps 0-3, 4-7  softmax of tile (or stream) 0, 1: one row per thread.  p =
+//                   2^(s - m) with m raised only when a row's logit exceeds it
+//                   by more than 2^8 (the warp then rescales its rows of O in
+//                   tensor memory; the products that wrote them were issued
+//                   before the ones that made S, so they are complete).  P
 //                   overwrites S as bf16.  No barrier among warps: a row
 //                   belongs to one thread from the scores to the output.
 //   warp 8          schedule and TMA: Q once per unit, K_i, V_i through a ring
 //   warp 9          issues the products
+//
+// What bounds it: an iteration of two tiles costs the tensor cores 2 x (512 +
+// 512) cycles at their peak rate, and 256 KB of shared-memory traffic (both
+// operands of Q K^T, V, and the tiles coming in), 2048 cycles as well; the
+// kernel takes about 3200.  Long prompts run into the 1000 W power cap (1.05
+// PFLOP/s at 1.5 GHz for 4096 tokens over 28k, 1.2 PFLOP/s before the clock
+// drops), short ones into what starting and ending a unit costs, a few tokens
+// over a long context and single tokens into HBM (5.2 and 5.5 TB/s).  Tried
+// and slower: half a row per thread with sixteen softmax warps (2.05 against
+// 1.97 ms), a quarter or half of the exponentials as a polynomial on the
+// multiply-add pipe (2.03, 2.19 ms).
 //
 // Work split.  The iterations of all units, laid end to end, are cut into
 // equal shares, one per CTA (one CTA per SM), so that ragged lengths, causal
@@ -100,6 +114,7 @@ struct SlotNote {
 // sequence's start have no key and still need their outputs).
 struct SeqUnits {
   int64_t c, count, len;   // c = len - count
+  int64_t first;           // first packed row
   int32_t ks;
   __host__ __device__ int64_t units() const { return (count + (int64_t(1) << ks) - 1) >> ks; }
   __host__ __device__ int64_t iters(int64_t u) const {
@@ -145,8 +160,16 @@ __device__ __forceinline__ SeqUnits seq_units(const PromptArgs& a, int64_t b, in
                                               bool reporter) {
   SeqUnits s;
   s.ks = ks;
-  s.count = a.cu != nullptr ? int64_t(__ldg(a.cu + b + 1)) - __ldg(a.cu + b) : 1;
-  if (s.count < 0) s.count = 0;
+  s.first = b;
+  s.count = 1;
+  if (a.cu != nullptr) {
+    // rows outside [0, n_tokens) are nobody's, whatever cu_tokens says
+    const int64_t c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+    s.first = c0 < 0 ? 0 : (c0 > a.n_tokens ? a.n_tokens : c0);
+    const int64_t end = c1 > a.n_tokens ? a.n_tokens : c1;
+    s.count = end > s.first ? end - s.first : 0;
+    if (reporter && (c0 != s.first || c1 != s.first + s.count)) report(a.status, COBS_ERR_DEVICE);
+  }
   s.len = __ldg(a.seq_lens + b);
   if (s.len < 0 || s.len > a.max_seq_len) {
     if (reporter && s.count > 0) report(a.status, COBS_ERR_DEVICE);
@@ -397,7 +420,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       Segment g;
       g.b = b;
       g.h = h;
-      g.tok0 = (a.cu != nullptr ? int64_t(__ldg(a.cu + b)) : int64_t(b)) + int64_t(u) * k_unit;
+      g.tok0 = su.first + int64_t(u) * k_unit;
       g.pos0 = su.c + int64_t(u) * k_unit;
       g.len = su.len;
       const int64_t rest = su.count - int64_t(u) * k_unit;

@@ -21,7 +21,9 @@
  * sequence after the other; cu_tokens (device int32 [batch + 1], ascending
  * from 0) gives sequence b the rows [cu_tokens[b], cu_tokens[b + 1]).  A
  * sequence may have no row.  Rows at or past cu_tokens[batch] belong to
- * nobody: they are not read and their outputs are left as they were.
+ * nobody: they are not read and their outputs are left as they were.  Bounds
+ * that point outside [0, n_tokens] are cut to it (cobs_prompt_attention
+ * reports them as COBS_ERR_DEVICE).
  * cu_tokens NULL: one token per sequence, n_tokens == batch. */
 #ifndef COBS_CACHE_H_
 #define COBS_CACHE_H_
@@ -174,7 +176,7 @@ COBS_API size_t cobs_prompt_workspace_bytes(const cobs_dims* dims, int64_t n_tok
  * A row with a negative position (more rows than tokens) attends to nothing:
  * out 0, lse -inf.  Keys and values at or past a sequence's length are never
  * read into a result, whatever they hold.  Keys and values inside a sequence
- * must be finite: a value that is not may also reach rows up to 127 tokens
+ * must be finite: a value that is not may also reach rows up to 382 tokens
  * before it.  A block inside a sequence whose page is missing or >= n_pages
  * counts as tokens that are not there, and is reported as COBS_ERR_DEVICE.
  *   ws           at least cobs_prompt_workspace_bytes(dims, n_tokens,
@@ -198,7 +200,7 @@ COBS_API cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_
  * to 2^-16 of the row's largest (components below it are rounded by at most
  * 2^-24 of the largest), and each weight e^(logit_j - m) v_scale_j rounded by
  * at most 2^-16 of itself or 2^-22 of the pair's largest, whichever is more.
- * Codes of tokens inside a sequence must not be NaN.
+ * Queries must be finite, and codes of tokens inside a sequence not NaN.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 COBS_API cobs_status cobs_sparse_decode_cache(const cobs_dims* dims, const cobs_kv_cache* cache,
                                               const void* q, const int32_t* idx,

@@ -109,6 +109,35 @@ def test_prompt(lens, paged):
         p.check(lse=i % 3 != 2)
 
 
+@pytest.mark.parametrize("paged", [False, True])
+def test_many_units_per_cta(paged):
+    """More units than CTAs: whole ones of short sequences (single tokens and
+    prompts mixed), and equal shares of long ones that cut units anywhere."""
+    short = [(b * 37) % 300 + 1 for b in range(130)]
+    mixed = ([1 if b % 3 else min(n, (b * 13) % 70) for b, n in enumerate(short)], short)
+    for heads, lens in (((8, 8, 64), (None, short)), ((16, 4, 128), mixed), ((4, 4, 64), mixed),
+                        ((16, 2, 128), ([1999, 700, 1, 350], [2100, 1500, 4000, 350])),
+                        ((8, 8, 128), ([1111, 2], [1700, 3000])),
+                        ((4, 2, 64), ([900, 2048, 17], [5000, 2048, 1100]))):
+        p = Prompt(heads, lens, paged)
+        p.call()
+        assert p.status() == 0
+        p.check()
+
+
+def test_bounds_past_the_rows_are_cut_and_reported():
+    p = Prompt((8, 2, 128), ([30, 40, 20], [300, 333, 64]), False, pad=0)
+    p.cu[3] = 500                    # the last sequence claims rows that are not there
+    p.out = torch.full((200, 8, 128), -7.0, dtype=torch.bfloat16, device="cuda")
+    p.call()
+    assert p.status() == cb.COBS_ERR_DEVICE
+    p.check()
+    p.cu[0] = -5
+    p.call()
+    assert p.status() == cb.COBS_ERR_DEVICE
+    p.check()
+
+
 def test_sharp_and_flat_rows():
     """Logits up to some hundreds (weights of one key) and all equal."""
     for kscale in (30.0, 0.0):
