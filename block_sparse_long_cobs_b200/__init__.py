@@ -31,5 +31,7 @@ __all__ = [
 
 def __getattr__(name):
     if name in __all__:
-        return getattr(_import_module("._binding", __name__), name)
+        value = getattr(_import_module("._binding", __name__), name)
+        globals()[name] = value     # looked up once: a call must not pay for it again
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

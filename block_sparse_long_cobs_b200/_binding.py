@@ -437,16 +437,12 @@ def cobs_rope_init(rotary_dim, interleaved=False, base=10000.0, scaling=COBS_ROP
     return rope
 
 
-def _ref(x):
-    return None if x is None else ctypes.byref(x)
-
-
 def cobs_append_tokens(dims, cache, rope, q, q_stride, k, k_stride, v, v_stride, cu_tokens,
                        n_tokens, start, q_out, ws, ws_bytes, stream=None, check=True) -> int:
     """Rotate the packed new tokens' q and k and store their k and v in the cache.
     q, k and v may be parts of one fused projection (rows q_stride, ... apart);
     rope and q (with q_out) may be None."""
-    st = lib.cobs_append_tokens(ctypes.byref(_dims(dims)), _ref(cache), _ref(rope),
+    st = lib.cobs_append_tokens(_dims(dims), cache, rope,
                                 _rows_addr(q, q_stride, "q"), q_stride,
                                 _rows_addr(k, k_stride, "k"), k_stride,
                                 _rows_addr(v, v_stride, "v"), v_stride, _addr(cu_tokens),
@@ -459,7 +455,7 @@ def cobs_read_cache(dims, cache, seq_lens, block_begin, block_end, k_out, v_out,
                     stream=None, check=True) -> int:
     """Blocks of a cache of either format as bf16 pages (seq_lens, k_out or v_out
     may be None)."""
-    st = lib.cobs_read_cache(ctypes.byref(_dims(dims)), _ref(cache), _addr(seq_lens),
+    st = lib.cobs_read_cache(_dims(dims), cache, _addr(seq_lens),
                              block_begin, block_end, _addr(k_out), _addr(v_out), _addr(ws),
                              ws_bytes, _stream(stream))
     return _check("cobs_read_cache", st, check)
@@ -477,7 +473,7 @@ def cobs_prompt_attention(dims, cache, q, cu_tokens, n_tokens, seq_lens, max_seq
                           check=True) -> int:
     """Causal attention of the packed new tokens over the bf16 cache that holds
     them (cu_tokens None: one token per sequence; lse may be None)."""
-    st = lib.cobs_prompt_attention(ctypes.byref(_dims(dims)), _ref(cache), _addr(q),
+    st = lib.cobs_prompt_attention(_dims(dims), cache, _addr(q),
                                    _addr(cu_tokens), n_tokens, _addr(seq_lens), max_seq_len,
                                    softmax_scale, _addr(out), _addr(lse), _addr(ws), ws_bytes,
                                    _stream(stream))
@@ -489,7 +485,7 @@ def cobs_sparse_decode_cache(dims, cache, q, idx, n_sel, idx_stride, seq_lens, m
                              check=True) -> int:
     """cobs_sparse_decode over a cache of either format, contiguous or paged
     (seq_lens None: every sequence is max_seq_len tokens long)."""
-    st = lib.cobs_sparse_decode_cache(ctypes.byref(_dims(dims)), _ref(cache), _addr(q),
+    st = lib.cobs_sparse_decode_cache(_dims(dims), cache, _addr(q),
                                       _addr(idx), _addr(n_sel), idx_stride, _addr(seq_lens),
                                       max_seq_len, softmax_scale, _addr(out), _addr(lse),
                                       _addr(ws), ws_bytes, _stream(stream))
