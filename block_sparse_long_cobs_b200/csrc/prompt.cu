@@ -29,7 +29,7 @@
 // What bounds it: an iteration of two tiles costs the tensor cores 2 x (512 +
 // 512) cycles at their peak rate, and 256 KB of shared-memory traffic (both
 // operands of Q K^T, V, and the tiles coming in), 2048 cycles as well; the
-// kernel takes about 3200.  Long prompts run into the 1000 W power cap (1.05
+// kernel takes about 3500.  Long prompts run into the 1000 W power cap (1.05
 // PFLOP/s at 1.5 GHz for 4096 tokens over 28k, 1.2 PFLOP/s before the clock
 // drops), short ones into what starting and ending a unit costs, a few tokens
 // over a long context and single tokens into HBM (5.2 and 5.5 TB/s).  Tried

@@ -195,3 +195,51 @@ def test_wrong_memory_is_refused():
                                                         device="cuda"), None, s.ws, s.ws.numel())
     assert e.value.status == cb.COBS_ERR_INVALID_ARG
     assert "device pointer" in cb.cobs_last_error()
+
+
+def test_append_then_fused_selection_and_decode():
+    """Decode steps without a host wait between the calls: append, then the call
+    whose decode starts while the selection still runs, against the separate
+    calls on the same cache with the GPU idle in between."""
+    batch, cap, n0, hkv = 40, 1024, 700, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (bf16_rows(g, batch, hkv, cap, D) for _ in range(2))
+    dims = cb.cobs_dims(batch=batch, num_q_heads=4 * hkv, num_kv_heads=hkv, head_dim=D,
+                        block_size=B, rank=RANK, capacity_tokens=cap)
+    cache = cb.cobs_kv_cache(k, v)
+    rope = cb.cobs_rope_init(D, True)
+    stats = torch.zeros(batch, hkv, cap // B, (1 + RANK) * D, dtype=torch.bfloat16, device="cuda")
+    stride = cb.cobs_selected_capacity(dims, 3, 1, 64)
+    size = cb.cobs_workspace_bytes(dims, 3, 1, 64)
+    ws, ws2 = workspace(size), workspace(size)
+    cb.cobs_build_block_stats(dims, k, 0, n0 // B, stats, ws, size)
+
+    def buffers():
+        return (torch.zeros(batch, hkv, stride, dtype=torch.int32, device="cuda"),
+                torch.zeros(batch, hkv, dtype=torch.int32, device="cuda"),
+                torch.zeros(batch, 4 * hkv, D, device="cuda"),
+                torch.zeros(batch, 4 * hkv, device="cuda"))
+    steps = 6
+    qkv = [bf16_rows(g, batch, 6 * hkv, D, scale=2.0) for _ in range(steps)]
+    got = [buffers() for _ in range(steps)]
+    q = [torch.zeros(batch, 4 * hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+    torch.cuda.synchronize()
+    starts = [ints([n0 + t] * batch) for t in range(steps)]
+    torch.cuda.synchronize()
+    for t in range(steps):
+        x, wide = qkv[t], 6 * hkv * D
+        cb.cobs_append_tokens(dims, cache, rope, x[:, :4 * hkv], wide, x[:, 4 * hkv:5 * hkv], wide,
+                              x[:, 5 * hkv:], wide, None, batch, starts[t], q[t], ws, size)
+        idx, n_sel, out, lse = got[t]
+        cb.cobs_select_and_decode(dims, q[t], stats, k, v, n0 + t + 1, 3, 1, 64, SCALE, idx, stride,
+                                  n_sel, None, out, lse, ws, size)
+    assert cb.cobs_read_device_status(ws, size) == 0
+    for t in range(steps):
+        idx, n_sel, out, lse = buffers()
+        cb.cobs_select_blocks(dims, q[t], stats, n0 + t + 1, 3, 1, 64, idx, stride, n_sel, None,
+                              ws2, size)
+        torch.cuda.synchronize()
+        cb.cobs_sparse_decode_cache(dims, cache, q[t], idx, n_sel, stride, None, n0 + t + 1, SCALE,
+                                    out, lse, ws2, size)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[t], (idx, n_sel, out, lse)))
