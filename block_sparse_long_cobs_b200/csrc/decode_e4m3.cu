@@ -742,7 +742,8 @@ cudaError_t launch_g(DecodeArgs a, const float* ks, const float* vs, cudaStream_
   e = set_smem_attrs(kern, S::kDynSmem);
   if (e != cudaSuccess) return e;
   // the bf16 decode's split: a pair is cut only as far as the resident CTAs
-  // can still take every chunk in one wave, four blocks a chunk at least
+  // can still take every chunk in one wave, four blocks a chunk at least (one
+  // sequence of 4 pairs: 8.7 us with its lists cut, 256 whole pairs 24.3)
   int sms = device_sm_count();
   if (sms <= 0) sms = 148;
   const int64_t pairs = int64_t(a.batch) * a.hkv;

@@ -43,7 +43,10 @@
 // unit that a cut goes through leaves partial rows (o, m, l) in the workspace
 // (at most two per CTA), which prompt_merge_kernel joins.  With sequences of
 // at most kWholeTokens tokens the shares are whole units instead: cutting them
-// would cost more than it evens out.
+// costs more than it evens out (one prompt of 1000 tokens 24 us whole, 31 in
+// equal shares, 32 single tokens at 1000 tokens 31 and 40, eight prompts 122 and
+// 113; at 2000 tokens one prompt 68 and 59, four 215 and 169, 32 single tokens 52
+// and 60).
 //
 // Rows of the last block past a sequence's end are zeroed in the V tile after
 // it lands (a zero weight times a NaN is not zero); scores of keys past a
@@ -69,8 +72,12 @@ constexpr int kKeys = 1 << kKeyShift;    // keys per iteration
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kMaxCtas = 148;            // one per SM
 constexpr int64_t kWholeTokens = 1024;   // longest sequence whose units are never cut
-constexpr int kUnitCost = 2;             // what starting and ending a unit costs, in iterations
-constexpr int kMinShare = 4;             // iterations of a share, at least
+// What starting and ending a unit costs, in iterations: ragged prompts of up to
+// 4099 tokens took 419, 386, 399 and 398 us with 1, 2, 3 and 4.
+constexpr int kUnitCost = 2;
+// Iterations of a share, at least: 16 tokens at 2000 took 14.2, 15.8 and 19.0 us
+// with 2, 4 and 8, two single tokens at 4000 18.6, 18.2 and 20.4.
+constexpr int kMinShare = 4;
 constexpr int kSegQ = 2;                 // segments handed from the producer to the others
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kTmemCols = 512;      // S0, S1 (P over them), O0, O1
@@ -559,9 +566,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return warp_wait(bar, parity, a.status, &abort_s);
     };
-    // (a descriptor's address field counts 16 bytes; shared memory ends
-    // below 2^18, so adding to it never carries out of its 14 bits)
-    // S of stream wc = Q of tile qt times the keys in ring slot st
+    // S of stream wc = Q of tile qt times the keys in ring slot st.  (A
+    // descriptor's address field counts 16 bytes; shared memory ends below
+    // 2^18, so adding to it never carries out of its 14 bits.)
     auto qk = [&](auto wc, int qt, uint32_t st) {
       constexpr int w = decltype(wc)::value;
       const uint64_t qd = umma_desc_sw128(q0 + qt * T::kBytes);
@@ -574,6 +581,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       umma_commit_if(elected, &s_full[w]);
       issued = true;
     };
+    // O += P V over one tile's keys, a half as soon as its weights are there
     auto pv = [&](auto wc, uint32_t st, uint32_t accumulate, uint32_t parity) {
       constexpr int w = decltype(wc)::value;
       const uint64_t vd = umma_desc_sw128_mn(ring0 + st * T::kBytes, T::kSlabBytes);
