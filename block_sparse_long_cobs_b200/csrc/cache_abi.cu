@@ -249,10 +249,20 @@ static cobs_status check_prompt_sizes(const cobs_dims* dims, int64_t n_tokens,
   return COBS_OK;
 }
 
+// The split rows lie where the selection and the decode keep scores and their
+// own partial rows, behind the counters that those calls leave for the next
+// one: a workspace may serve them all.
+static size_t prompt_partials_at(const cobs_dims* dims) { return layout(dims, 0).scores; }
+
+static size_t prompt_need(const cobs_dims* dims, int64_t n_tokens, int64_t max_seq_len) {
+  const size_t rows = prompt_partial_bytes(dims, n_tokens, max_seq_len);
+  return rows == 0 ? kStatusBytes : prompt_partials_at(dims) + rows;
+}
+
 size_t cobs_prompt_workspace_bytes(const cobs_dims* dims, int64_t n_tokens, int64_t max_seq_len) {
   if (check_prompt_sizes(dims, n_tokens, max_seq_len) != COBS_OK) return 0;
   ok();
-  return kStatusBytes + prompt_partial_bytes(dims, n_tokens, max_seq_len);
+  return prompt_need(dims, n_tokens, max_seq_len);
 }
 
 cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_cache* cache,
@@ -274,8 +284,8 @@ cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_cache* ca
     return fail(COBS_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
   if (!(std::isfinite(softmax_scale)) || softmax_scale <= 0.f)
     return fail(COBS_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
-  const size_t need = kStatusBytes + prompt_partial_bytes(dims, n_tokens, max_seq_len);
-  if ((st = check_ws(ws, ws_bytes, need)) != COBS_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, prompt_need(dims, n_tokens, max_seq_len))) != COBS_OK)
+    return st;
   if (n_tokens == 0) return ok();
   if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
   if ((st = check_device("q", q)) != COBS_OK) return st;
@@ -286,7 +296,7 @@ cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_cache* ca
   a.seq_lens = seq_lens;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  a.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kStatusBytes);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + prompt_partials_at(dims));
   a.status = static_cast<int32_t*>(ws);
   a.n_tokens = n_tokens;
   a.max_seq_len = max_seq_len;

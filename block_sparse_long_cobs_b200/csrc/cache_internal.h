@@ -54,7 +54,7 @@ struct PromptArgs {
   const int64_t* seq_lens; // [batch]
   uint16_t* out;           // [n_tokens][hq][d]
   float* lse;              // [n_tokens][hq] or null
-  float* partials;         // split rows (PromptPlan)
+  float* partials;         // notes and rows of units that were cut
   int32_t* status;
   int64_t n_tokens, max_seq_len;
   int32_t batch, hq, d;

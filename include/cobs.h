@@ -193,7 +193,9 @@ COBS_API int32_t cobs_selected_capacity(const cobs_dims* dims, int32_t top_k,
  * and cobs_sparse_decode need for these settings (one workspace serves all
  * three; it does not depend on the device).  Returns 0 for invalid arguments.
  * The workspace holds a status word, per-(batch, kv-head) counters, block
- * scores and split-K partial results. */
+ * scores and split-K partial results; where the counters lie depends on batch
+ * and num_kv_heads, so that a workspace serves calls of one batch and one number
+ * of kv-heads (or is initialised again in between). */
 COBS_API size_t cobs_workspace_bytes(const cobs_dims* dims, int32_t top_k,
                             int32_t sink_blocks, int32_t local_tokens);
 

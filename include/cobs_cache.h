@@ -17,6 +17,14 @@
  * on the current device, which must be the one the pointers belong to.
  * The calls can be captured into CUDA graphs.
  *
+ * One workspace, initialised once with cobs_workspace_init, may serve all
+ * calls of the same batch and num_kv_heads, those of cobs.h among them, when it
+ * is as large as the largest of cobs_workspace_bytes and
+ * cobs_prompt_workspace_bytes asks for.  Where its counters lie depends on
+ * batch and num_kv_heads: selection, decode and prompt attention of another
+ * batch or other kv-heads need another workspace, or this one initialised
+ * again.  (cobs_append_tokens and cobs_read_cache use the status word alone.)
+ *
  * Packed tokens.  n_tokens rows hold the new tokens of all sequences, one
  * sequence after the other; cu_tokens (device int32 [batch + 1], ascending
  * from 0) gives sequence b the rows [cu_tokens[b], cu_tokens[b + 1]).  A
@@ -152,8 +160,9 @@ COBS_API cobs_status cobs_read_cache(const cobs_dims* dims, const cobs_kv_cache*
                                      size_t ws_bytes, void* stream);
 
 /* Bytes of workspace that cobs_prompt_attention needs for up to n_tokens
- * packed rows over sequences of up to max_seq_len tokens (the status word and
- * the partial results of split rows; it does not depend on the device).
+ * packed rows over sequences of up to max_seq_len tokens (the status word, room
+ * for the counters of the selection and the decode, and the partial results of
+ * split rows; it does not depend on the device).
  * Returns 0 (and sets the last error) for invalid arguments. */
 COBS_API size_t cobs_prompt_workspace_bytes(const cobs_dims* dims, int64_t n_tokens,
                                             int64_t max_seq_len);

@@ -2,6 +2,7 @@
 checks before any launch, and the rotary table (no GPU)."""
 
 import ctypes
+import itertools
 import math
 import os
 import re
@@ -130,6 +131,19 @@ def test_prompt_refusals():
     # a program may size its workspace once, for its largest call
     sizes = [cb.cobs_prompt_workspace_bytes(dims(), n, t) for n, t in ((1, 64), (1, 4096))]
     assert sizes == sorted(sizes)
+
+
+def test_prompt_partials_lie_behind_the_counters():
+    """One workspace may serve the prompt attention, the selection and the
+    decode: the split rows of the first leave the counters of the others alone,
+    which take 4 + 4 + 8 bytes per (sequence, kv-head)."""
+    for hkv in (2, 8):
+        need = [cb.cobs_prompt_workspace_bytes(
+            dims(batch=b, num_q_heads=4 * hkv, num_kv_heads=hkv), 100000, 4096)
+            for b in (1, 50, 2000)]
+        for (b0, n0), (b1, n1) in itertools.pairwise(zip((1, 50, 2000), need)):
+            # (each of the three arrays is padded to 256 bytes)
+            assert n1 - n0 >= 16 * hkv * (b1 - b0) - 3 * 256
 
 
 def decode(**kw):

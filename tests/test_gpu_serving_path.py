@@ -12,7 +12,8 @@ import pytest
 import torch
 
 import block_sparse_long_cobs_b200 as cb
-from cache_ref import B, attend, bf16_rows, cu_of, frequencies, ints, page_table, rotate, workspace
+from cache_ref import (B, attend, bf16_rows, cu_of, frequencies, ints, page_table, quantise,
+                       rotate, workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +244,70 @@ def test_append_then_fused_selection_and_decode():
                                     out, lse, ws2, size)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got[t], (idx, n_sel, out, lse)))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_one_workspace_for_every_call(e4m3):
+    """Prompt attention whose units are cut, selection, decode and the fused
+    call in turn on one workspace, against the same calls on workspaces of their
+    own: no call leaves the others' counters changed."""
+    batch, cap, hkv, hq = 8, 2048, 4, 16
+    g = torch.Generator(device="cuda").manual_seed(11)
+    k, v = (bf16_rows(g, batch, hkv, cap, D) for _ in range(2))
+    dims = cb.cobs_dims(batch=batch, num_q_heads=hq, num_kv_heads=hkv, head_dim=D, block_size=B,
+                        rank=RANK, capacity_tokens=cap)
+    cache = cb.cobs_kv_cache(k, v)
+    dcache = cache
+    if e4m3:
+        (kc, ks), (vc, vs) = quantise(k), quantise(v)
+        dcache = cb.cobs_kv_cache(kc, vc, ks, vs, format=cb.COBS_CACHE_E4M3)
+    counts, lens = [40, 1, 0, 200, 3, 17, 64, 5], [1500, 2048, 64, 1999, 1100, 700, 1280, 2000]
+    n, most = sum(counts), max(lens)
+    stats = torch.zeros(batch, hkv, cap // B, (1 + RANK) * D, dtype=torch.bfloat16, device="cuda")
+    stride = cb.cobs_selected_capacity(dims, 5, 1, 64)
+    size = cb.cobs_workspace_bytes(dims, 5, 1, 64)
+    psize = cb.cobs_prompt_workspace_bytes(dims, n, most)
+    cb.cobs_build_block_stats(dims, k, 0, cap // B, stats, workspace(), 256)
+    pq = bf16_rows(g, n, hq, D, scale=2.0)
+    q = bf16_rows(g, batch, hq, D, scale=2.0)
+    cu, sl = cu_of(counts), ints(lens)
+    torch.cuda.synchronize()
+
+    def step(ws_of):
+        out = torch.zeros_like(pq)
+        plse = torch.zeros(n, hq, device="cuda")
+        res = [out, plse]
+        ws = ws_of("prompt", psize)
+        cb.cobs_prompt_attention(dims, cache, pq, cu, n, sl, most, SCALE, out, plse, ws,
+                                 ws.numel())
+        for fused in (False, True):
+            idx = torch.zeros(batch, hkv, stride, dtype=torch.int32, device="cuda")
+            n_sel = torch.zeros(batch, hkv, dtype=torch.int32, device="cuda")
+            o = torch.zeros(batch, hq, D, device="cuda")
+            lse = torch.zeros(batch, hq, device="cuda")
+            ws = ws_of("fused" if fused else "select", size)
+            if fused:
+                cb.cobs_select_and_decode(dims, q, stats, k, v, 1900, 5, 1, 64, SCALE, idx, stride,
+                                          n_sel, None, o, lse, ws, ws.numel())
+            else:
+                cb.cobs_select_blocks(dims, q, stats, 1900, 5, 1, 64, idx, stride, n_sel, None, ws,
+                                      ws.numel())
+                ws = ws_of("decode", size)
+                cb.cobs_sparse_decode_cache(dims, dcache, q, idx, n_sel, stride, None, 1900, SCALE,
+                                            o, lse, ws, ws.numel())
+            res += [idx, n_sel, o, lse]
+        torch.cuda.synchronize()
+        return res
+
+    own = {}
+
+    def own_ws(name, nbytes):
+        own.setdefault(name, workspace(nbytes))
+        return own[name]
+    want = step(own_ws)
+    shared = workspace(max(size, psize))
+    for _ in range(4):
+        got = step(lambda name, nbytes: shared)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for ws in [shared, *own.values()]:
+        assert cb.cobs_read_device_status(ws, ws.numel()) == 0
