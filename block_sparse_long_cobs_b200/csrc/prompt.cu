@@ -793,6 +793,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             const bool raise = mx > m + kRescaleLog2;
             sure = __any_sync(0xffffffffu, raise);
             if (!sure) break;
+            // the weights that were stored with the old maximum are in place
+            // before the new ones go to the same columns (two stores are not
+            // ordered by themselves)
+            tmem_wait_st();
             const float mn = raise ? mx : m;
             const float alpha = raise ? hw_exp2(m - mn) : 1.f;   // 0 while m is -inf
             m = mn;

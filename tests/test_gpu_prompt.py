@@ -162,6 +162,31 @@ def test_rising_logits():
         p.check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_maximum_that_moves_at_every_tile(d):
+    """Every tile's logits lie 16 above those of the tile before, so that each
+    row's weights are formed twice at each tile: with two tiles a unit, with one,
+    and one row, always the same answer."""
+    for heads, lens in (((8, 1, d), ([40, 17], [2500, 700])), ((1, 1, d), ([300], [1900])),
+                        ((8, 2, d), ([1, 1], [3000, 129]))):
+        p = Prompt(heads, lens, False)
+        for b, n in enumerate(lens[1]):
+            step = torch.arange(n, device="cuda") // 128 * 16.0
+            p.cache.parts["k"][b, :, :n] *= 0.25
+            p.cache.parts["k"][b, :, :n, 0] = (step / (4.0 * p.scale)).bfloat16()
+        p.q[:p.n] *= 0.25
+        p.q[:p.n, :, 0] = 4.0
+        p.call()
+        assert p.status() == 0
+        p.check()
+        first = p.out.clone(), p.lse.clone()
+        for _ in range(20):
+            p.call()
+            assert torch.equal(p.out[:p.n], first[0][:p.n])
+            assert torch.equal(p.lse[:p.n], first[1][:p.n])
+        assert p.status() == 0
+
+
 def test_lengths_outside_the_bound_are_clamped_and_reported():
     for bad, used in ((-3, 0), (500, 333)):
         p = Prompt((4, 1, 64), ([10, 20], [100, 333]), False)
