@@ -850,10 +850,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         tc_fence_after();
         const bool mine = tok < ntok;
         const float mm = fmaxf(m, m1);
-        const bool some = mm != -INFINITY;           // the row has a key
         const float w0 = m != -INFINITY ? hw_exp2(m - mm) : 0.f;
         const float w1 = m1 != -INFINITY ? hw_exp2(m1 - mm) : 0.f;
         const float ll = l * w0 + l1 * w1;
+        // whether the row has a key is asked of the sum: a NaN among its scores
+        // leaves the maximum alone (it may still be -inf), and must come out
+        const bool some = ll != 0.f;
         const float inv = type == kWhole ? (some ? 1.f / ll : 0.f) : 1.f;
         const float f0 = w0 * inv, f1 = w1 * inv;
         const int64_t r = (tok0 + tok) * a.hq + head0 + (row & (group - 1));
@@ -911,7 +913,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (mine && type == kWhole) {
           if (a.lse != nullptr) a.lse[r] = some ? (mm + log2f(ll)) * kLn2 : -INFINITY;
         } else if (mine) {
-          part[kUnitRows * D + pr] = mm;
+          // (a row of NaN: with a finite maximum the merge cannot drop it)
+          part[kUnitRows * D + pr] = isnan(ll) ? 0.f : mm;
           part[kUnitRows * (D + 1) + pr] = ll;
         }
         tc_fence_before();

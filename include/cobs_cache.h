@@ -183,11 +183,15 @@ COBS_API size_t cobs_prompt_workspace_bytes(const cobs_dims* dims, int64_t n_tok
  *   out          device bf16 [n_tokens][num_q_heads][d]
  *   lse          device fp32 [n_tokens][num_q_heads] or NULL
  * A row with a negative position (more rows than tokens) attends to nothing:
- * out 0, lse -inf.  Keys and values at or past a sequence's length are never
- * read into a result, whatever they hold.  Keys and values inside a sequence
- * must be finite: a value that is not may also reach rows up to 382 tokens
- * before it.  A block inside a sequence whose page is missing or >= n_pages
- * counts as tokens that are not there, and is reported as COBS_ERR_DEVICE.
+ * out 0, lse -inf.  A row one of whose logits is NaN or +inf (its query, or a
+ * product with it, is not finite) is NaN in out and lse; one whose logits are
+ * all -inf is as one without keys.  Keys and values at or past a sequence's
+ * length are never read into a result, whatever they hold.  Keys and values
+ * inside a sequence must be finite: a value that is not may also reach rows up
+ * to 382 tokens before it.  A block inside a sequence whose page is missing or
+ * >= n_pages counts as tokens that are not there, and is reported as
+ * COBS_ERR_DEVICE.  Weights are rounded to bf16 before they meet the values
+ * (2^-9 of each at most), not before they are summed.
  *   ws           at least cobs_prompt_workspace_bytes(dims, n_tokens,
  *                max_seq_len), initialised once with cobs_workspace_init;
  *                calls that share it must not overlap on the GPU

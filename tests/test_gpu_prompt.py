@@ -291,3 +291,46 @@ def test_rows_equal_the_sparse_decode_over_all_blocks():
     assert cb.cobs_read_device_status(ws, wsb) == 0
     assert (lse - p.lse).abs().max() <= 2.0 ** -11
     assert ((out - p.out.float()).abs() <= 2.0 ** -6 * out.abs().amax() + 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_query_that_is_not_finite(bad):
+    """Its row is NaN, in out and lse, wherever it lies: in a first tile that is
+    partly masked, in a later one, in a unit of one tile or two, whole or cut;
+    every other row is what it was, bit for bit.  A row that attends to nothing
+    stays 0 and -inf."""
+    for heads, lens, rows in (((4, 1, 64), "short", (5, 76)),
+                              ((8, 2, 128), "tiles", (50, 130, 700)),
+                              ((8, 1, 128), "few_long", (0, 2, 4)),
+                              ((8, 8, 128), "chunk", (0, 137, 299)),
+                              ((16, 2, 64), "singles", (2, 3)),
+                              ((4, 4, 64), ([900, 2048, 17], [5000, 2048, 1100]),
+                               (3, 899, 950, 2000, 2964)),
+                              ((4, 2, 128), "more_rows_than_tokens", (0, 40, 71))):
+        p = Prompt(heads, lens, True)
+        p.call()
+        assert p.status() == 0
+        clean = p.out.clone(), p.lse.clone()
+        hit = torch.zeros(p.rows, p.hq, dtype=torch.bool, device="cuda")
+        for i, r in enumerate(rows):
+            h = (3 * i + 1) % p.hq
+            p.q[r, h, (11 * i) % p.d] = bad
+            # (not where the row has no key)
+            first = [sum(p.counts[:b]) for b in range(len(p.counts) + 1)]
+            b = max(b for b in range(len(p.counts)) if first[b] <= r)
+            hit[r, h] = p.lens[b] - p.counts[b] + r - first[b] >= 0
+        if bad == math.inf:
+            # a logit of +inf for every key that such a row sees
+            for b in range(len(p.lens)):
+                k = p.cache.parts["k"]
+                k.abs_()
+            p.q.abs_()
+            clean = None
+        p.call()
+        assert p.status() == 0
+        assert torch.isnan(p.out[hit]).all() and torch.isnan(p.lse[hit]).all()
+        n = slice(0, p.n)
+        assert not torch.isnan(p.out[n][~hit[n]]).any() and not torch.isnan(p.lse[n][~hit[n]]).any()
+        if clean:
+            assert torch.equal(p.out[~hit], clean[0][~hit])
+            assert torch.equal(p.lse[~hit], clean[1][~hit])
