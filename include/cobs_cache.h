@@ -191,7 +191,7 @@ COBS_API size_t cobs_prompt_workspace_bytes(const cobs_dims* dims, int64_t n_tok
  * to 382 tokens before it.  A block inside a sequence whose page is missing or
  * >= n_pages counts as tokens that are not there, and is reported as
  * COBS_ERR_DEVICE.  Weights are rounded to bf16 before they meet the values
- * (2^-9 of each at most), not before they are summed.
+ * (off by 2^-8 of each at most), not before they are summed.
  *   ws           at least cobs_prompt_workspace_bytes(dims, n_tokens,
  *                max_seq_len), initialised once with cobs_workspace_init;
  *                calls that share it must not overlap on the GPU
