@@ -8,7 +8,7 @@
 //
 // Operands.  A query row times a power of two is split into three E4M3 parts,
 // q = h0 + h1 / 16 + h2 / 256 (a part takes 4 significant bits; the last one's
-// smallest step is 2^-25 of the row's largest), so that S = K [h0; h1; h2]^T
+// smallest step is 2^-23 to 2^-24 of the row's largest), so that S = K [h0; h1; h2]^T
 // (M = 128 keys) loses nothing of a bf16 query.  The weights of the values,
 // w = vs 2^(s - M), are split into four parts in the same way (2^-16 of the
 // weight, 2^-22 of the largest), and O^T = V^T [w0; w1; w2; w3]^T (M = 128
@@ -320,7 +320,9 @@ decode_e4m3_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             uint32_t code[3];
-            split2<3>(x[2 * u] * sc, x[2 * u + 1] * sc, code);
+            // x 0 is NaN for what is not finite: its code must not saturate
+            split2<3>(fmaf(x[2 * u], 0.f, x[2 * u] * sc),
+                      fmaf(x[2 * u + 1], 0.f, x[2 * u + 1] * sc), code);
 #pragma unroll
             for (int p = 0; p < 3; ++p) (u < 2 ? lo[p] : hi[p]) |= (code[p] & 0xffffu) << (16 * (u & 1));
           }
@@ -467,7 +469,9 @@ decode_e4m3_kernel(const __grid_constant__ CUtensorMap kmap,
           float* part = a.partials + (hq0 + h) * hstride + int64_t(pg.seg) * (a.d + 2);
           if (r < a.d) part[r] = ov;
           if (r == h) {
-            part[a.d] = pm[h];
+            // (a row of NaN, whose maximum may be -inf: with a finite one the
+            // merge cannot drop it)
+            part[a.d] = isnan(l) ? 0.f : pm[h];
             part[a.d + 1] = l;
           }
         }
@@ -721,8 +725,8 @@ __global__ void __launch_bounds__(D) merge_rows_kernel(const DecodeArgs a) {
       O = w > 0.f ? fmaf(w, o[u], O) : O;
     }
   }
-  a.out[hq * D + r] = L > 0.f ? O / L : 0.f;
-  if (r == 0) a.lse[hq] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  a.out[hq * D + r] = L != 0.f ? O / L : 0.f;   // (not L > 0: NaN stays)
+  if (r == 0) a.lse[hq] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 template <int G>

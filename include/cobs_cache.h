@@ -213,7 +213,9 @@ COBS_API cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_
  * to 2^-16 of the row's largest (components below it are rounded by at most
  * 2^-24 of the largest), and each weight e^(logit_j - m) v_scale_j rounded by
  * at most 2^-16 of itself or 2^-22 of the pair's largest, whichever is more.
- * Queries must be finite, and codes of tokens inside a sequence not NaN.
+ * A query row with a component that is not finite is NaN in out and lse.  Codes
+ * of tokens inside a sequence must not be NaN, and their scales finite and
+ * >= 0.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 COBS_API cobs_status cobs_sparse_decode_cache(const cobs_dims* dims, const cobs_kv_cache* cache,
                                               const void* q, const int32_t* idx,

@@ -223,3 +223,25 @@ def test_graph_replay_and_stream():
         torch.cuda.synchronize()
         assert p.status() == 0
         p.check()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("heads", [(4, 1, 64), (8, 2, 128), (2, 2, 128), (16, 2, 128)])
+def test_query_that_is_not_finite(heads, bad):
+    """Its row is NaN, in out and lse, whether the pair's list is one chunk of
+    work or cut and merged; every other row is what it was, bit for bit."""
+    for lens, n_sel in (([4000], 40), ([700] * 160, 4), ([100, 1], 2)):
+        p = Decode(heads, lens, n_sel, True)
+        p.call()
+        assert p.status() == 0
+        clean = p.out.clone(), p.lse.clone()
+        hit = torch.zeros(len(lens), p.hq, dtype=torch.bool, device="cuda")
+        for i, b in enumerate({0, len(lens) // 2, len(lens) - 1}):
+            h = (2 * i + 1) % p.hq
+            p.q[b, h, (p.d - 1) // (i + 1)] = bad
+            hit[b, h] = True
+        p.call()
+        assert p.status() == 0
+        assert torch.isnan(p.out[hit]).all() and torch.isnan(p.lse[hit]).all()
+        assert torch.equal(p.out[~hit], clean[0][~hit])
+        assert torch.equal(p.lse[~hit], clean[1][~hit])
