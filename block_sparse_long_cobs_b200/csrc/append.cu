@@ -41,9 +41,16 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
   const int64_t token = item / a.chunks;
+  // bounds outside the rows, or descending, are reported: the first warps look
+  // at 32 sequences each
+  if (a.cu != nullptr)
+    for (int64_t s = item * 32 + lane; s < a.batch; s += int64_t(gridDim.x) * kAppendWarps * 32) {
+      const int64_t c0 = __ldg(a.cu + s), c1 = __ldg(a.cu + s + 1);
+      if (c0 < 0 || c1 < c0 || c1 > a.n_tokens) report(a.status, COBS_ERR_DEVICE);
+    }
   if (token >= a.n_tokens) return;
   int b;
-  int64_t pos;
+  int64_t pos, first = token;            // of the sequence, its bound cut to the rows
   if (a.cu != nullptr && a.batch <= 32) {
     // bounds and lengths of all sequences at once: one trip to memory, not two
     const bool in = lane < a.batch;
@@ -51,12 +58,15 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
     const int64_t st = in ? __ldg(a.start + lane) : 0;
     b = __popc(__ballot_sync(0xffffffffu, in && int64_t(c1) <= token));
     if (b >= a.batch) return;
-    pos = __shfl_sync(0xffffffffu, st, b) + token - __shfl_sync(0xffffffffu, c0, b);
+    first = max(__shfl_sync(0xffffffffu, c0, b), 0);
+    pos = __shfl_sync(0xffffffffu, st, b) + token - first;
   } else {
     b = warp_find_sequence(a.cu, a.batch, token, lane);
     if (b >= a.batch) return;
-    pos = __ldg(a.start + b) + (a.cu != nullptr ? token - __ldg(a.cu + b) : 0);
+    if (a.cu != nullptr) first = max(__ldg(a.cu + b), 0);
+    pos = __ldg(a.start + b) + token - first;
   }
+  if (token < first) return;             // before the first bound: nobody's
   const int hkv = a.c.hkv;
   const int n_rows = a.hq + 2 * hkv;
   const int r0 = int(item % a.chunks) * a.rows_per_warp;

@@ -28,10 +28,10 @@
  * Packed tokens.  n_tokens rows hold the new tokens of all sequences, one
  * sequence after the other; cu_tokens (device int32 [batch + 1], ascending
  * from 0) gives sequence b the rows [cu_tokens[b], cu_tokens[b + 1]).  A
- * sequence may have no row.  Rows at or past cu_tokens[batch] belong to
- * nobody: they are not read and their outputs are left as they were.  Bounds
- * that point outside [0, n_tokens] are cut to it (cobs_prompt_attention
- * reports them as COBS_ERR_DEVICE).
+ * sequence may have no row.  Rows before cu_tokens[0] and rows at or past
+ * cu_tokens[batch] belong to nobody: they reach no result and their outputs are
+ * left as they were.  Bounds that point outside [0, n_tokens] are cut to it, and
+ * reported as COBS_ERR_DEVICE, as are bounds that descend.
  * cu_tokens NULL: one token per sequence, n_tokens == batch. */
 #ifndef COBS_CACHE_H_
 #define COBS_CACHE_H_

@@ -218,6 +218,62 @@ def test_append_outside_the_cache_is_reported(e4m3):
         p.check(f, inter, amp)
 
 
+@pytest.mark.parametrize("extra", [0, 40])
+def test_append_bounds_outside_the_rows_are_cut_and_reported(extra):
+    """Bounds below 0 and past n_tokens, with few sequences and with more than a
+    warp has lanes: every row is stored where the bounds cut to [0, n_tokens]
+    put it."""
+    counts, starts = [5, 0, 9] + [1] * extra, [60, 7, 0] + [3] * extra
+    for first, last in ((-5, None), (None, 7), (-1, 1000), (None, None)):
+        p = Append((4, 1, 64), counts, starts, False, True, pad=0)
+        r, f, inter, amp = make_rope(ROPES["half"], 64)
+        if first is not None:
+            p.cu[0] = first
+        if last is not None:
+            p.cu[-1] += last
+        bad = first is not None or last is not None
+        assert p.call(r) == (cb.COBS_ERR_DEVICE if bad else 0)
+        p.check(f, inter, amp)
+
+
+@pytest.mark.parametrize("extra", [0, 40])
+def test_append_rows_before_the_first_bound_are_nobodys(extra):
+    """cu_tokens[0] > 0: the rows before it are neither stored nor rotated."""
+    counts, starts = [5, 9] + [1] * extra, [60, 70] + [3] * extra
+    p = Append((4, 1, 64), counts, starts, False, True, pad=0)
+    r, f, inter, amp = make_rope(ROPES["half"], 64)
+    cut = 2
+    p.cu[0] = cut
+    assert p.call(r) == 0
+    assert (p.q_out[:cut] == -7).all()
+    # what is left of the first sequence starts at its first position
+    p.pos[cut:5] -= cut
+    p.qkv, p.q_out, p.pos, p.seq = p.qkv[cut:], p.q_out[cut:], p.pos[cut:], p.seq[cut:]
+    p.n -= cut
+    p.check(f, inter, amp)
+
+
+@pytest.mark.parametrize("batch", [31, 32, 33])
+def test_append_around_a_warp_of_sequences(batch):
+    """Batches about as large as a warp, empty sequences at the ends."""
+    counts = [(5 * b + 1) % 4 for b in range(batch)]
+    counts[0] = counts[-1] = 0
+    starts = [(29 * b) % 130 for b in range(batch)]
+    p = Append((8, 2, 128), counts, starts, False, True)
+    r, f, inter, amp = make_rope(ROPES["inter"], 128)
+    assert p.call(r) == 0
+    p.check(f, inter, amp)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_with_given_frequencies(interleaved):
+    want = [3.0, 0.0, 1.0, 0.31, 1e-3, 2.0 ** -20, 0.7, 1e-9]
+    p = Append((4, 1, 64), [5, 9], [100000, 0], False, True)
+    r = cb.cobs_rope_init(16, interleaved, scaling=cb.COBS_ROPE_CUSTOM, frequencies=want)
+    assert p.call(r) == 0
+    p.check(torch.tensor(want, dtype=torch.float64, device="cuda"), interleaved, 1.0)
+
+
 def test_append_zero_tiny_and_non_finite_rows():
     """E4M3: zero rows, rows below the smallest scale, huge rows, NaN and
     infinities."""
