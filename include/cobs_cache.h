@@ -54,10 +54,11 @@ extern "C" {
  *   block_table   device int32 [batch][table_stride]: the page of block j of
  *                 sequence b; a negative entry is a block without a page
  * An E4M3 row (one token of one kv-head) stores scale = max |x| / 448 over
- * its finite components, and per component the code of x / scale, rounded to
- * nearest, ties to even; the value it stands for is code * scale.  A row
- * whose largest finite magnitude is below 448 * 2^-126 stores scale 0 and
- * zero codes; a component that is not finite stores the NaN code. */
+ * its finite components, and per component the code of the fp32 quotient
+ * x / scale, rounded to nearest, ties to even; the value it stands for is
+ * code * scale.  A row whose largest finite magnitude is below 448 * 2^-126
+ * stores scale 0 and zero codes; a component that is not finite stores the NaN
+ * code. */
 typedef struct cobs_kv_cache {
   void* k;
   void* v;

@@ -274,6 +274,29 @@ def test_append_with_given_frequencies(interleaved):
     p.check(torch.tensor(want, dtype=torch.float64, device="cuda"), interleaved, 1.0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_codes_are_those_of_the_quotient(d):
+    """E4M3 values are not rotated, so that their scales and codes are those of
+    max |x| / 448 and x / scale in fp32, each rounded once, bit for bit: quotients
+    that lie on or beside the middle of two codes among them."""
+    p = Append((1, 1, d), [2000, 300], [0, 64], True, False)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows = torch.randint(128, 256, (p.rows, 1, d), generator=g, device="cuda").float() / 128.0
+    rows *= 2.0 ** torch.randint(-6, 1, (p.rows, 1, d), generator=g, device="cuda").float()
+    rows *= torch.randint(0, 2, (p.rows, 1, d), generator=g, device="cuda").float() * 2 - 1
+    rows *= 2.0 ** torch.tensor([0.0, -115.0, -70.0, 60.0], device="cuda").repeat(
+        p.rows // 4 + 1)[:p.rows, None, None]
+    rows[0, 0, 0], rows[0, 0, 1:] = 1.078125, 0.80859375     # a quotient of 336, a tie
+    p.qkv[:, 2:] = rows.bfloat16()
+    assert (p.qkv[:, 2:].float() == rows).all()
+    assert p.call(None) == 0
+    scale = rows[:p.n, 0].abs().amax(-1).cpu() / 448.0
+    code = (rows[:p.n, 0].cpu() / scale[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    at = p.where()
+    assert torch.equal(p.vs[at][:, 0].cpu(), scale)
+    assert torch.equal(p.v[at][:, 0].cpu(), code)
+
+
 def test_append_zero_tiny_and_non_finite_rows():
     """E4M3: zero rows, rows below the smallest scale, huge rows, NaN and
     infinities."""
