@@ -2,6 +2,7 @@
 // and launch arguments.  Everything that can be checked on the host is
 // checked here, before any CUDA call.
 #include <cmath>
+#include <initializer_list>
 
 #include "abi_common.h"
 #include "cache_internal.h"
@@ -69,24 +70,34 @@ cobs_status check_rows(const char* name, const void* p, int64_t stride, int64_t 
   return COBS_OK;
 }
 
-// Whether p is memory of the current device, or memory that it can reach: the
-// last check before a launch (a host pointer, or another device's, would
-// fault in the kernel).
-cobs_status check_device(const char* name, const void* p) {
+// Whether every buffer of a call (null: not given) is memory of the current
+// device, or memory that it can reach: the last check before a launch.  A host
+// pointer, or another device's, would fault in the kernel.
+struct Buffer {
+  const char* name;
+  const void* p;
+};
+cobs_status check_device(std::initializer_list<Buffer> buffers) {
   int dev = 0;
-  cudaPointerAttributes at{};
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, p);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();   // not sticky: leave no error behind
-    return fail(COBS_ERR_INVALID_ARG, "%s is not a device pointer", name);
+  bool known = cudaGetDevice(&dev) == cudaSuccess;
+  for (const Buffer& x : buffers) {
+    if (!x.p) continue;
+    cudaPointerAttributes at{};
+    known = known && cudaPointerGetAttributes(&at, x.p) == cudaSuccess;
+    if (!known || at.type == cudaMemoryTypeUnregistered) {
+      (void)cudaGetLastError();   // not sticky: leave no error behind
+      return fail(COBS_ERR_INVALID_ARG, "%s is not a device pointer", x.name);
+    }
+    if (at.type == cudaMemoryTypeDevice && at.device != dev)
+      return fail(COBS_ERR_INVALID_ARG, "%s lies on device %d, the current device is %d", x.name,
+                  at.device, dev);
   }
-  if (at.type == cudaMemoryTypeUnregistered)
-    return fail(COBS_ERR_INVALID_ARG, "%s is not a device pointer", name);
-  if (at.type == cudaMemoryTypeDevice && at.device != dev)
-    return fail(COBS_ERR_INVALID_ARG, "%s lies on device %d, the current device is %d", name,
-                at.device, dev);
   return COBS_OK;
+}
+
+// A cache's scales, where its format has them.
+const void* scale_of(const cobs_kv_cache* c, const float* s) {
+  return c->format == COBS_CACHE_E4M3 ? s : nullptr;
 }
 
 }  // namespace
@@ -179,8 +190,12 @@ cobs_status cobs_append_tokens(const cobs_dims* dims, const cobs_kv_cache* cache
   }
   if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != COBS_OK) return st;
   if (n_tokens == 0) return ok();
-  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
-  if ((st = check_device("k", k)) != COBS_OK) return st;
+  st = check_device({{"cache k", cache->k}, {"cache v", cache->v},
+                     {"k_scale", scale_of(cache, cache->k_scale)},
+                     {"v_scale", scale_of(cache, cache->v_scale)},
+                     {"block_table", cache->block_table}, {"q", q}, {"k", k}, {"v", v},
+                     {"cu_tokens", cu_tokens}, {"start", start}, {"q_out", q_out}, {"ws", ws}});
+  if (st != COBS_OK) return st;
   AppendArgs a{};
   a.c = view_of(dims, cache);
   if (rope) a.rope = *rope;
@@ -219,8 +234,12 @@ cobs_status cobs_read_cache(const cobs_dims* dims, const cobs_kv_cache* cache,
     return fail(COBS_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
   if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != COBS_OK) return st;
   if (block_end == block_begin) return ok();
-  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
-  if ((st = check_device("k_out or v_out", k_out ? k_out : v_out)) != COBS_OK) return st;
+  st = check_device({{"cache k", cache->k}, {"cache v", cache->v},
+                     {"k_scale", scale_of(cache, cache->k_scale)},
+                     {"v_scale", scale_of(cache, cache->v_scale)},
+                     {"block_table", cache->block_table}, {"seq_lens", seq_lens},
+                     {"k_out", k_out}, {"v_out", v_out}, {"ws", ws}});
+  if (st != COBS_OK) return st;
   ReadArgs a{};
   a.c = view_of(dims, cache);
   a.seq_lens = seq_lens;
@@ -287,8 +306,10 @@ cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_cache* ca
   if ((st = check_ws(ws, ws_bytes, prompt_need(dims, n_tokens, max_seq_len))) != COBS_OK)
     return st;
   if (n_tokens == 0) return ok();
-  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
-  if ((st = check_device("q", q)) != COBS_OK) return st;
+  st = check_device({{"cache k", cache->k}, {"cache v", cache->v},
+                     {"block_table", cache->block_table}, {"q", q}, {"cu_tokens", cu_tokens},
+                     {"seq_lens", seq_lens}, {"out", out}, {"lse", lse}, {"ws", ws}});
+  if (st != COBS_OK) return st;
   PromptArgs a{};
   a.c = view_of(dims, cache);
   a.q = static_cast<const uint16_t*>(q);
@@ -325,8 +346,13 @@ cobs_status cobs_sparse_decode_cache(const cobs_dims* dims, const cobs_kv_cache*
                    cache->n_pages, idx, n_sel, idx_stride, seq_lens, max_seq_len, softmax_scale,
                    out, lse, ws, ws_bytes, &a);
   if (st != COBS_OK) return st;
-  if ((st = check_device("cache k", cache->k)) != COBS_OK) return st;
-  if ((st = check_device("q", q)) != COBS_OK) return st;
+  st = check_device({{"cache k", cache->k}, {"cache v", cache->v},
+                     {"k_scale", scale_of(cache, cache->k_scale)},
+                     {"v_scale", scale_of(cache, cache->v_scale)},
+                     {"block_table", cache->block_table}, {"q", q}, {"idx", idx},
+                     {"n_sel", n_sel}, {"seq_lens", seq_lens}, {"out", out}, {"lse", lse},
+                     {"ws", ws}});
+  if (st != COBS_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->format == COBS_CACHE_BF16
                             ? launch_decode(a, s)

@@ -14,7 +14,9 @@
  * caller owns all memory, nothing is allocated), host checks before any
  * launch, the status word of the workspace, cobs_last_error(), 16-byte
  * alignment of every device pointer, and thread safety.  The kernels launch
- * on the current device, which must be the one the pointers belong to.
+ * on the current device, which must be the one the pointers belong to: a
+ * buffer that begins in another device's memory, or in host memory that the
+ * CUDA runtime does not know, is refused (INVALID_ARG).
  * The calls can be captured into CUDA graphs.
  *
  * One workspace, initialised once with cobs_workspace_init, may serve all

@@ -311,3 +311,37 @@ def test_one_workspace_for_every_call(e4m3):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     for ws in [shared, *own.values()]:
         assert cb.cobs_read_device_status(ws, ws.numel()) == 0
+
+
+def test_every_buffer_in_host_memory_is_refused():
+    """A host address in place of any buffer of a call: INVALID_ARG, no launch."""
+    host = torch.zeros(1 << 16, dtype=torch.uint8).data_ptr() + 15 & ~15
+    dev = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda").data_ptr()
+    dims = cb.cobs_dims(batch=2, num_q_heads=4, num_kv_heads=1, head_dim=64, block_size=B, rank=0,
+                        capacity_tokens=64)
+    rope = cb.cobs_rope_init(64)
+
+    def append(c, q, k, v, cu, start, out, ws):
+        cb.cobs_append_tokens(dims, c, rope, q, 256, k, 64, v, 64, cu, 2, start, out, ws, 1 << 16)
+
+    def read(c, lens, k, v, ws):
+        cb.cobs_read_cache(dims, c, lens, 0, 1, k, v, ws, 1 << 16)
+
+    def prompt(c, q, cu, lens, out, lse, ws):
+        cb.cobs_prompt_attention(dims, c, q, cu, 2, lens, 64, SCALE, out, lse, ws, 1 << 16)
+
+    def decode(c, q, idx, n, lens, out, lse, ws):
+        cb.cobs_sparse_decode_cache(dims, c, q, idx, n, 1, lens, 64, SCALE, out, lse, ws, 1 << 16)
+    for fn, n, formats in ((append, 7, (0, 1)), (read, 4, (0, 1)), (prompt, 6, (0,)),
+                           (decode, 7, (0, 1))):
+        for fmt in formats:
+            for bad in range(n + 5):
+                if fmt == 0 and bad in (2, 3):        # scales of a bf16 cache: not looked at
+                    continue
+                at = [host if i == bad else dev for i in range(n + 5)]
+                cache = cb.cobs_kv_cache(*at[:5], n_pages=1, table_stride=1, format=fmt)
+                with pytest.raises(cb.CobsError) as e:
+                    fn(cache, *at[5:])
+                assert e.value.status == cb.COBS_ERR_INVALID_ARG, (fn.__name__, bad)
+                assert "not a device pointer" in cb.cobs_last_error()
+    torch.cuda.synchronize()
