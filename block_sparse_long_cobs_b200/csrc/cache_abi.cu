@@ -46,11 +46,18 @@ CacheView view_of(const cobs_dims* dims, const cobs_kv_cache* c) {
   return v;
 }
 
+// Number of packed rows.
+cobs_status check_count(const cobs_dims* dims, int64_t n_tokens) {
+  if (n_tokens < 0) return fail(COBS_ERR_INVALID_ARG, "n_tokens must be >= 0");
+  if (n_tokens > (kMaxRows - 1) / (int64_t(dims->num_q_heads) + 2 * int64_t(dims->num_kv_heads)))
+    return fail(COBS_ERR_UNSUPPORTED, "n_tokens * head rows must be < 2^31");
+  return COBS_OK;
+}
+
 // Packed rows of new tokens.
 cobs_status check_tokens(const cobs_dims* dims, const int32_t* cu_tokens, int64_t n_tokens) {
-  if (n_tokens < 0) return fail(COBS_ERR_INVALID_ARG, "n_tokens must be >= 0");
-  if (n_tokens * (int64_t(dims->num_q_heads) + 2 * dims->num_kv_heads) >= kMaxRows)
-    return fail(COBS_ERR_UNSUPPORTED, "n_tokens * head rows must be < 2^31");
+  const cobs_status st = check_count(dims, n_tokens);
+  if (st != COBS_OK) return st;
   if (cu_tokens && !aligned16(cu_tokens))
     return fail(COBS_ERR_INVALID_ARG, "cu_tokens must be 16-byte aligned");
   if (!cu_tokens && n_tokens != dims->batch)
@@ -259,9 +266,7 @@ static cobs_status check_prompt_sizes(const cobs_dims* dims, int64_t n_tokens,
                                       int64_t max_seq_len) {
   cobs_status st = check_dims(dims);
   if (st != COBS_OK) return st;
-  if (n_tokens < 0) return fail(COBS_ERR_INVALID_ARG, "n_tokens must be >= 0");
-  if (n_tokens * (int64_t(dims->num_q_heads) + 2 * dims->num_kv_heads) >= kMaxRows)
-    return fail(COBS_ERR_UNSUPPORTED, "n_tokens * head rows must be < 2^31");
+  if ((st = check_count(dims, n_tokens)) != COBS_OK) return st;
   if (max_seq_len < 1 || max_seq_len > dims->capacity_tokens)
     return fail(COBS_ERR_INVALID_ARG, "max_seq_len %lld outside [1, capacity_tokens]",
                 (long long)max_seq_len);

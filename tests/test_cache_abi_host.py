@@ -133,6 +133,15 @@ def test_prompt_refusals():
     assert sizes == sorted(sizes)
 
 
+def test_token_counts_that_overflow_are_refused():
+    """Products with the head counts would wrap around to nothing."""
+    for n in (1 << 62, (1 << 63) - 1, (1 << 64) // 12 + 1, (1 << 31) // 12 + 1):
+        for fn in (append, prompt):
+            refuse(UNS, fn, n_tokens=n)
+        with pytest.raises(cb.CobsError):
+            cb.cobs_prompt_workspace_bytes(dims(), n, 64)
+
+
 def test_prompt_partials_lie_behind_the_counters():
     """One workspace may serve the prompt attention, the selection and the
     decode: the split rows of the first leave the counters of the others alone,
