@@ -175,16 +175,18 @@ cobs_status cobs_append_tokens(const cobs_dims* dims, const cobs_kv_cache* cache
   if ((st = check_cache(dims, cache, 0)) != COBS_OK) return st;
   const int64_t kv_row = int64_t(dims->num_kv_heads) * dims->head_dim;
   const int64_t q_row = int64_t(dims->num_q_heads) * dims->head_dim;
-  if ((st = check_rows("k", k, k_stride, kv_row)) != COBS_OK) return st;
-  if ((st = check_rows("v", v, v_stride, kv_row)) != COBS_OK) return st;
-  if (q) {
-    if ((st = check_rows("q", q, q_stride, q_row)) != COBS_OK) return st;
-    if (!q_out || !aligned16(q_out))
-      return fail(COBS_ERR_INVALID_ARG, "q_out must not be NULL and must be 16-byte aligned");
-    if (q_out == q && q_stride != q_row)
-      return fail(COBS_ERR_INVALID_ARG, "in place, q_stride must be num_q_heads * head_dim");
-  } else if (q_out) {
-    return fail(COBS_ERR_INVALID_ARG, "q_out without q");
+  if (n_tokens > 0) {   // (empty tensors have no address)
+    if ((st = check_rows("k", k, k_stride, kv_row)) != COBS_OK) return st;
+    if ((st = check_rows("v", v, v_stride, kv_row)) != COBS_OK) return st;
+    if (q) {
+      if ((st = check_rows("q", q, q_stride, q_row)) != COBS_OK) return st;
+      if (!q_out || !aligned16(q_out))
+        return fail(COBS_ERR_INVALID_ARG, "q_out must not be NULL and must be 16-byte aligned");
+      if (q_out == q && q_stride != q_row)
+        return fail(COBS_ERR_INVALID_ARG, "in place, q_stride must be num_q_heads * head_dim");
+    } else if (q_out) {
+      return fail(COBS_ERR_INVALID_ARG, "q_out without q");
+    }
   }
   if (!start || !aligned16(start))
     return fail(COBS_ERR_INVALID_ARG, "start must not be NULL and must be 16-byte aligned");
@@ -235,7 +237,8 @@ cobs_status cobs_read_cache(const cobs_dims* dims, const cobs_kv_cache* cache,
     return fail(COBS_ERR_INVALID_ARG, "block range [%lld, %lld) outside [0, %lld]",
                 (long long)block_begin, (long long)block_end, (long long)nb_cap);
   if ((st = check_cache(dims, cache, block_end)) != COBS_OK) return st;
-  if (!k_out && !v_out) return fail(COBS_ERR_INVALID_ARG, "k_out and v_out are both NULL");
+  if (!k_out && !v_out && block_end > block_begin)
+    return fail(COBS_ERR_INVALID_ARG, "k_out and v_out are both NULL");
   if ((k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)) ||
       (seq_lens && !aligned16(seq_lens)))
     return fail(COBS_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
@@ -302,7 +305,7 @@ cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_cache* ca
     return fail(COBS_ERR_UNSUPPORTED,
                 "prompt attention reads a bf16 cache: read an E4M3 cache back with "
                 "cobs_read_cache first");
-  if (!q || !seq_lens || !out)
+  if (!seq_lens || (n_tokens > 0 && (!q || !out)))
     return fail(COBS_ERR_INVALID_ARG, "q, seq_lens and out must not be NULL");
   if (!aligned16(q) || !aligned16(seq_lens) || !aligned16(out) || (lse && !aligned16(lse)))
     return fail(COBS_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");

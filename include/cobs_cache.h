@@ -34,7 +34,8 @@
  * cu_tokens[batch] belong to nobody: they reach no result and their outputs are
  * left as they were.  Bounds that point outside [0, n_tokens] are cut to it, and
  * reported as COBS_ERR_DEVICE, as are bounds that descend.
- * cu_tokens NULL: one token per sequence, n_tokens == batch. */
+ * cu_tokens NULL: one token per sequence, n_tokens == batch.  With n_tokens 0
+ * (or no blocks to read) nothing is done, and buffers of rows may be NULL. */
 #ifndef COBS_CACHE_H_
 #define COBS_CACHE_H_
 
@@ -217,8 +218,8 @@ COBS_API cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_
  * 2^-24 of the largest), and each weight e^(logit_j - m) v_scale_j rounded by
  * at most 2^-16 of itself or 2^-22 of the pair's largest, whichever is more.
  * A query row with a component that is not finite is NaN in out and lse.  Codes
- * of tokens inside a sequence must not be NaN, and their scales finite and
- * >= 0.
+ * of tokens inside a sequence must not be NaN, and their scales must be as
+ * cobs_append_tokens stores them: 0, or finite and at least 2^-126.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 COBS_API cobs_status cobs_sparse_decode_cache(const cobs_dims* dims, const cobs_kv_cache* cache,
                                               const void* q, const int32_t* idx,

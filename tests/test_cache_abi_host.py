@@ -142,6 +142,17 @@ def test_token_counts_that_overflow_are_refused():
             cb.cobs_prompt_workspace_bytes(dims(), n, 64)
 
 
+def test_empty_calls_need_no_buffers_of_rows():
+    """No token, no block: an empty tensor has no address, and nothing is done."""
+    append(n_tokens=0, q=None, k=None, v=None, q_out=None)
+    append(n_tokens=0, q=A, k=None, v=None, q_out=None)
+    prompt(n_tokens=0, q=None, out=None, lse=None)
+    read(block_begin=2, block_end=2, k_out=None, v_out=None)
+    for kw in (dict(start=None), dict(ws_bytes=8), dict(cache=cache(k=None))):
+        with pytest.raises(cb.CobsError):
+            append(n_tokens=0, k=None, v=None, q=None, q_out=None, **kw)
+
+
 def test_prompt_partials_lie_behind_the_counters():
     """One workspace may serve the prompt attention, the selection and the
     decode: the split rows of the first leave the counters of the others alone,
