@@ -216,7 +216,7 @@ COBS_API cobs_status cobs_prompt_attention(const cobs_dims* dims, const cobs_kv_
  * with q split into three E4M3 parts that hold every component exactly down
  * to 2^-16 of the row's largest (components below it are rounded by at most
  * 2^-24 of the largest), and each weight e^(logit_j - m) v_scale_j rounded by
- * at most 2^-16 of itself or 2^-22 of the pair's largest, whichever is more.
+ * at most 2^-16 of itself or 2^-24 of the pair's largest, whichever is more.
  * A query row with a component that is not finite is NaN in out and lse.  Codes
  * of tokens inside a sequence must not be NaN, and their scales must be as
  * cobs_append_tokens stores them: 0, or finite and at least 2^-126.

@@ -245,3 +245,37 @@ def test_query_that_is_not_finite(heads, bad):
         assert torch.isnan(p.out[hit]).all() and torch.isnan(p.lse[hit]).all()
         assert torch.equal(p.out[~hit], clean[0][~hit])
         assert torch.equal(p.lse[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 1, 64), (4, 4, 128)])
+def test_small_weights_beside_a_large_one(heads):
+    """One key's weight is 2^8 to 2^13 times that of a thousand others, which are
+    all alike, so that whatever their rounding loses adds up: at most 2^-16 of
+    each (four parts) or 2^-24 of the largest (the unit is at most a quarter of
+    it, and the last part's step 2^-21 of the unit), whichever is more."""
+    def prep(k, v):
+        k.zero_()
+        k[:, :, 3, 0] = 20.0
+        v[:, :, 4:] = v[:, :, 4:5]
+    # (so many pairs that none is cut)
+    p = Decode(heads, [1024, 1000, 777] * (56 // heads[1]) + [900] * 6, 16, False, prep=prep)
+    n = p.q.shape[0] * p.q.shape[1]
+    ramp = torch.linspace(3.0, 5.0, n, device="cuda").view(p.q.shape[:2])
+    p.q[..., 0] = (ramp * math.sqrt(p.d / 128)).bfloat16()
+    p.call()
+    assert p.status() == 0
+    p.check()
+    group = p.hq // p.hkv
+    for b, n in enumerate(p.lens):
+        for h in range(p.hkv):
+            k, v = (p.cache.rows(x, b, h, n) for x in "kv")
+            q = p.q[b, h * group:(h + 1) * group].double()
+            want, lse, w = attend(q, k, v, p.scale)
+            prob = torch.exp(q @ k.T * p.scale - lse[:, None])
+            vs = p.cache.scales("v", b, h, n)
+            codes = torch.where(vs[:, None] > 0, v / vs[:, None], 0.0)
+            big = float(q.norm(dim=-1).max() * k.norm(dim=-1).max()) * p.scale
+            tol = (2.0 ** -16 + 2.0 ** -18 + 2.0 ** -20 * big) * w \
+                + 2.0 ** -24 * (prob * vs).amax(1, keepdim=True) * codes.abs().sum(0)
+            err = (p.out[b, h * group:(h + 1) * group].double() - want).abs()
+            assert (err <= tol).all(), float((err / tol).max())
