@@ -27,12 +27,13 @@
 //   warp 9          issues the products
 //
 // What bounds it: an iteration of two tiles costs the tensor cores 2 x (512 +
-// 512) cycles at their peak rate, and 256 KB of shared-memory traffic (both
-// operands of Q K^T, V, and the tiles coming in), 2048 cycles as well; the
-// kernel takes about 3500.  Long prompts run into the 1000 W power cap (1.05
-// PFLOP/s at 1.5 GHz for 4096 tokens over 28k, 1.2 PFLOP/s before the clock
-// drops), short ones into what starting and ending a unit costs, a few tokens
-// over a long context and single tokens into HBM (5.2 and 5.5 TB/s).  Tried
+// 512) cycles at their peak rate, 256 KB of shared-memory traffic (both
+// operands of Q K^T, V, and the tiles coming in), 2048 cycles as well, and 2 x
+// 128 x 128 exponentials at 16 a cycle, 2048 too; the kernel takes about 3500.
+// Long prompts run into the 1000 W power cap (0.99 to 1.05 PFLOP/s at 1.5 GHz
+// for 4096 tokens over 28k, 1.2 PFLOP/s before the clock drops), short ones
+// into what starting and ending a unit costs, a few tokens over a long context
+// and single tokens into HBM (4.9 to 5.2 and 5.1 to 5.5 TB/s).  Tried
 // and slower: half a row per thread with sixteen softmax warps (2.05 against
 // 1.97 ms), a quarter or half of the exponentials as a polynomial on the
 // multiply-add pipe (2.03, 2.19 ms).
@@ -72,8 +73,13 @@ constexpr int kKeys = 1 << kKeyShift;    // keys per iteration
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kMaxCtas = 148;            // one per SM
 constexpr int64_t kWholeTokens = 1024;   // longest sequence whose units are never cut
-// What starting and ending a unit costs, in iterations: ragged prompts of up to
-// 4099 tokens took 419, 386, 399 and 398 us with 1, 2, 3 and 4.
+// What starting and ending a unit costs, in iterations.  us with 1, 2, 3 and 4,
+// six ragged prompts of up to 4099 tokens:
+//   d 128: 32 + 8 heads 391, 347, 353, 358; 64 + 8 762, 719, 704, 735; 8 + 8 123,
+//          122, 122, 122
+//   d 64:  16 + 16 heads 181, 182, 178, 178; 32 + 4 294, 287, 291, 301
+// 1500 tokens over 500 57.2, 56.9, 56.4, 55.2; four of 300 over 3000 62.3, 61.8,
+// 62.2, 62.7; twenty of 700 over 1500 (16 + 4) 121, 119, 119, 120.
 constexpr int kUnitCost = 2;
 // Iterations of a share, at least: 16 tokens at 2000 took 14.2, 15.8 and 19.0 us
 // with 2, 4 and 8, two single tokens at 4000 18.6, 18.2 and 20.4.
