@@ -374,3 +374,35 @@ def test_read_cache_pages_missing_or_outside_the_pool():
         assert cb.cobs_read_device_status(ws, 256) == want
         assert (out[1] == -7).all()
         assert torch.isfinite(out[[0, 2, 3]]).all() and (out[[0, 2, 3]] != -7).any()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_and_read_back_in_a_graph(e4m3):
+    """A captured decode step (append, read the blocks back), replayed from another
+    stream with new tokens at new positions, as its inputs are then."""
+    p = Append((8, 2, 128), None, [3, 70, 0, 130], e4m3, False)
+    r, f, inter, amp = make_rope(ROPES["half"], 128)
+    nb, wide, start = p.k.shape[2] // B, 12 * 128, ints(p.starts)
+    out = torch.zeros(4 * nb, 2, B, 128, dtype=torch.bfloat16, device="cuda")
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        cb.cobs_append_tokens(p.dims, p.cache, r, p.qkv[:, :8], wide, p.qkv[:, 8:10], wide,
+                              p.qkv[:, 10:], wide, None, 4, start, p.q_out, p.ws, 256, stream=s)
+        cb.cobs_read_cache(p.dims, p.cache, None, 0, nb, None, out, p.ws, 256, stream=s)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    for step in range(3):
+        p.qkv.copy_(bf16_rows(g, 4, 12, 128, scale=2.0))
+        start.copy_(ints([x + 7 * step for x in (3, 70, 0, 130)]))
+        graph.replay()
+        torch.cuda.synchronize()
+        p.pos = start.clone()
+        at = p.where()
+        v = p.v[at]
+        want = v.view(torch.float8_e4m3fn).float() * p.vs[at][..., None] if e4m3 \
+            else v.view(torch.bfloat16)
+        page, row = torch.arange(4, device="cuda") * nb + p.pos // B, p.pos % B
+        assert torch.equal(out[page, :, row], want.bfloat16())
+        p.check(f, inter, amp)      # (which puts the rows back as they were)
+    assert cb.cobs_read_device_status(p.ws, 256) == 0
